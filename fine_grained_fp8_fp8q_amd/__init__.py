@@ -27,6 +27,10 @@ Functions (names follow the C ABI without the ``fp8q_`` prefix):
 * ``gather_rows(codes, scales, index)`` -> (codes, scales) of rows ``index``
 * ``swiglu_quantize(x, scale_mode=..., cache=False, cache_scale_mode="pow2")``
   -> (codes, scales[, cache_codes, cache_scales])
+* the expert layer around the GEMMs: ``moe_sort`` (routing table),
+  ``moe_combine`` / ``moe_combine_backward`` (weighted sum of a token's
+  expert rows and its gradient), ``swiglu_backward`` (from the BF16 input or
+  its FP8 cache) and ``grouped_wgrad`` (every expert's weight gradient)
 """
 
 import ctypes
@@ -40,11 +44,13 @@ SCALE_FREE, SCALE_POW2 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 ACC_FP32, ACC_FP8_MFMA, ACC_FP8_MFMA_SCALED, ACC_FP32_POW2 = 0, 1, 2, 3
 TILE_ROW, TILE_TOKEN_T = 0, 1
+INDEX_I32, INDEX_I64 = 0, 1
 
 SYMBOLS = ("fp8q_quantize_act", "fp8q_quantize_weight", "fp8q_quantize_linear", "fp8q_quantize_weight_t", "fp8q_gemm",
            "fp8q_gemm_ex", "fp8q_gemm_quantized", "fp8q_grouped_gemm", "fp8q_grouped_gemm_ex", "fp8q_wgrad",
-           "fp8q_wgrad_ex", "fp8q_gather_rows", "fp8q_swiglu_quantize", "fp8q_set_gemm_small_limit",
-           "fp8q_status_string")
+           "fp8q_wgrad_ex", "fp8q_gather_rows", "fp8q_swiglu_quantize", "fp8q_moe_sort", "fp8q_moe_combine",
+           "fp8q_moe_combine_backward", "fp8q_swiglu_backward", "fp8q_grouped_wgrad", "fp8q_grouped_wgrad_ex",
+           "fp8q_moe_sort_workspace", "fp8q_set_gemm_small_limit", "fp8q_status_string")
 
 _lib = None
 
@@ -78,9 +84,18 @@ def load_library(path=None):
     lib.fp8q_wgrad_ex.argtypes = [vp, vp, vp, vp, i64, i64, i64, ip, vp, i64, vp]
     lib.fp8q_gather_rows.argtypes = [vp, i64, i64, i64, vp, vp, i64, vp, i64, vp, vp]
     lib.fp8q_swiglu_quantize.argtypes = [vp, i64, i64, i64, ip, vp, i64, vp, ip, vp, i64, vp, vp]
+    lib.fp8q_moe_sort.argtypes = [vp, ip, i64, i64, i64, i64, i32, i32, i64, vp, vp, vp, vp, i64, vp]
+    lib.fp8q_moe_combine.argtypes = [vp, ip, i64, i64, i64, vp, vp, i64, i64, ip, vp, i64, vp]
+    lib.fp8q_moe_combine_backward.argtypes = [vp, ip, i64, i64, i64, vp, ip, i64, i64, vp, vp, i64, vp, vp, i64, ip,
+                                              vp, i64, vp, vp, vp]
+    lib.fp8q_swiglu_backward.argtypes = [vp, vp, i64, i64, i64, vp, i64, vp, i64, ip, vp, i64, vp, vp, i64, vp]
+    lib.fp8q_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, i64, vp]
+    lib.fp8q_grouped_wgrad_ex.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, ip, vp, i64, vp]
+    lib.fp8q_moe_sort_workspace.argtypes = [i64, i64, i32]
+    lib.fp8q_moe_sort_workspace.restype = i64
     lib.fp8q_set_gemm_small_limit.argtypes = [i64]
     lib.fp8q_set_gemm_small_limit.restype = i64
-    for name in SYMBOLS[:-2]:
+    for name in SYMBOLS[:-3]:
         getattr(lib, name).restype = ctypes.c_int
     lib.fp8q_status_string.argtypes = [ctypes.c_int]
     lib.fp8q_status_string.restype = ctypes.c_char_p
@@ -126,8 +141,9 @@ def _need(t, dtype, name):
 
 def _row_major(t, name):
     """Row stride of a 2-D tensor with contiguous rows (any stride is fine for
-    an empty one: nothing is read through it)."""
-    if t.dim() != 2 or (t.numel() and t.stride(1) != 1):
+    an empty one: nothing is read through it; a single column has no column
+    stride)."""
+    if t.dim() != 2 or (t.numel() and t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
     return t.stride(0) if t.numel() else max(t.shape[1], 1)
 
@@ -450,3 +466,261 @@ def swiglu_quantize(x, scale_mode="free", cache=False, cache_scale_mode="pow2"):
         _ptr(cs) if cache else ctypes.c_void_p(0), _stream(x))
     _check(st, "fp8q_swiglu_quantize")
     return (codes, scales, cc, cs) if cache else (codes, scales)
+
+
+# ------------------------------------- the expert layer around the GEMMs ----
+
+def _one_device(first, *others):
+    """The device of the tensors given (None among them is skipped)."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
+    return dev
+
+
+def _call(dev, name, *args):
+    """Calls the entry point on the current stream of dev, which becomes the
+    current device for the call where it is not."""
+    torch = _torch()
+    fn = getattr(load_library(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != OK:
+        raise Fp8qError(st, name)
+
+
+def _addr(t):
+    """Address of a tensor's data, None (NULL) for none and for an empty one."""
+    return t.data_ptr() if t is not None and t.numel() else None
+
+
+def _ld(t, width):
+    """Row stride of a 2-D tensor that may be absent or empty; the stride of
+    a single row says nothing, and a stride below the width (an expanded or
+    overlapping tensor) is left for the library to refuse."""
+    return t.stride(0) if t is not None and t.numel() and t.shape[0] > 1 else max(width, 1)
+
+
+def _float_rows(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    code = _out_code(t.dtype)
+    _row_major(t, name)
+    return code
+
+
+def _pair_table(row_of, weights):
+    torch = _torch()
+    _need(row_of, torch.int32, "row_of")
+    if row_of.dim() != 2 or not row_of.is_contiguous():
+        raise ValueError("row_of must be a contiguous int32 [tokens, topk] tensor")
+    if weights is not None:
+        _contig_f32(weights, "weights")
+        if weights.shape != row_of.shape:
+            raise ValueError("weights must have the shape of row_of")
+
+
+def _own_rows(out, shape, dtype, device, name):
+    """A new [rows, cols] tensor, or the caller's if it has that form."""
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(out, dtype, name)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(out.shape)}")
+    _row_major(out, name)
+    return out
+
+
+def moe_sort(experts, num_hosted, first=0, align=1, rows_cap=None):
+    """Routing table of the experts first .. first + num_hosted - 1 from the
+    expert of every (token, choice) pair, int32 or int64 [tokens, topk].
+
+    Returns (offsets int32 [num_hosted + 1], token int32 [rows_cap], row_of
+    int32 [tokens, topk]): the groups' row ranges (padded to multiples of
+    align), the token of every row (-1 for padding and behind the last group;
+    ``gather_rows`` takes it as its index) and the row of every pair (-1: not
+    hosted here, or dropped).  rows_cap defaults to the smallest multiple of
+    align that drops no pair whatever the routing; pairs past a smaller one
+    are dropped.
+    """
+    torch = _torch()
+    if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
+        raise TypeError("experts must be an int32 or int64 tensor")
+    if not experts.is_cuda:
+        raise ValueError("experts must be on the GPU")
+    _row_major(experts, "experts")
+    tokens, topk = experts.shape
+    if num_hosted < 0 or align < 1:
+        raise ValueError("num_hosted must not be negative, align must be at least 1")
+    if rows_cap is None:
+        rows_cap = (tokens * topk + num_hosted * (align - 1) + align - 1) // align * align
+    dev = experts.device
+    # one allocation: [offsets | token | row_of], each part 16-byte aligned
+    n0, n1 = (num_hosted + 4) // 4 * 4, (rows_cap + 3) // 4 * 4
+    need = load_library().fp8q_moe_sort_workspace(tokens, topk, num_hosted)
+    n2 = (tokens * topk + 3) // 4 * 4 if need else tokens * topk
+    buf = torch.empty(n0 + n1 + n2 + need // 4, dtype=torch.int32, device=dev)
+    if num_hosted == 0:  # nothing is launched: every pair is without a row
+        buf.fill_(-1)
+        buf[0] = 0
+    p = buf.data_ptr()
+    _call(dev, "fp8q_moe_sort", _addr(experts), INDEX_I64 if experts.dtype == torch.int64 else INDEX_I32, tokens, topk,
+          _ld(experts, topk), first, num_hosted, align, rows_cap, p, p + 4 * n0, p + 4 * (n0 + n1),
+          p + 4 * (n0 + n1 + n2) if need else None, need)
+    return (buf[:num_hosted + 1], buf[n0:n0 + rows_cap],
+            buf[n0 + n1:n0 + n1 + tokens * topk].view(tokens, topk))
+
+
+def moe_combine(y, row_of, weights=None, out_dtype=None, out=None):
+    """out[t] = sum_j weights[t, j] * y[row_of[t, j]] in float32, rounded once.
+
+    y BF16 or float32 [rows_cap, N], row_of int32 [tokens, topk] (rows outside
+    y add nothing), weights float32 like row_of or None for the plain sum
+    (the gradient of the row gather).  out_dtype torch.bfloat16 (default) or
+    torch.float32.
+    """
+    torch = _torch()
+    yd = _float_rows(y, "y")
+    _pair_table(row_of, weights)
+    cap, n = y.shape
+    tokens, topk = row_of.shape
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out has another type than out_dtype")
+    dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    od = _out_code(dtype)
+    out = _own_rows(out, (tokens, n), dtype, y.device, "out")
+    dev = _one_device(y, row_of, weights, out)
+    _call(dev, "fp8q_moe_combine", _addr(y), yd, cap, n, _ld(y, n), _addr(row_of), _addr(weights), tokens, topk, od,
+          _addr(out), _ld(out, n))
+    return out
+
+
+def moe_combine_backward(dout, y, row_of, weights=None, token=None, bf16=True, quantize=False, scale_mode="free",
+                         want_dweights=True):
+    """Gradient of ``moe_combine`` for dout (BF16 or float32 [tokens, N]).
+
+    Returns (dy, codes, scales, dweights), None for what was not asked for:
+    dy BF16 [rows_cap, N] (bf16=True), its 1x128 quantization (quantize=True)
+    and float32 dweights [tokens, topk].  token is ``moe_sort``'s: rows
+    without a pair are zero; without it they are left uninitialised.
+    """
+    torch = _torch()
+    dd = _float_rows(dout, "dout")
+    yd = _float_rows(y, "y")
+    _pair_table(row_of, weights)
+    tokens, topk = row_of.shape
+    cap, n = y.shape
+    if tuple(dout.shape) != (tokens, n):
+        raise ValueError(f"dout must be [{tokens}, {n}], got {tuple(dout.shape)}")
+    if token is not None:
+        _need(token, torch.int32, "token")
+        if token.dim() != 1 or token.numel() != cap or not token.is_contiguous():
+            raise ValueError(f"token must be a contiguous int32 tensor of {cap} rows")
+    dev = _one_device(y, dout, row_of, weights, token)
+    dy = torch.empty((cap, n), dtype=torch.bfloat16, device=dev) if bf16 else None
+    codes = scales = dw = None
+    if quantize:
+        codes = _alloc_codes(cap, n, dev)
+        scales = torch.empty((cap, (n + 127) // 128), dtype=torch.float32, device=dev)
+    if want_dweights:
+        dw = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+    _call(dev, "fp8q_moe_combine_backward", _addr(dout), dd, tokens, n, _ld(dout, n), _addr(y), yd, cap,
+          _ld(y, n), _addr(row_of), _addr(weights), topk, _addr(token), _addr(dy), _ld(dy, n),
+          _scale_mode(scale_mode), _addr(codes), _ld(codes, n), _addr(scales), _addr(dw))
+    return dy, codes, scales, dw
+
+
+def swiglu_backward(x, dy, x_scales=None, bf16=True, quantize=False, scale_mode="pow2", want_y=False):
+    """Gradient of SwiGLU for x = [gate | up] and dy (BF16 [rows, inter]).
+
+    x is BF16 [rows, 2*inter], or uint8 E4M3 codes with x_scales [rows,
+    2*inter/128] (the cache of ``swiglu_quantize(cache=True)``).  Returns (dx,
+    y, codes, scales), None for what was not asked for: dx BF16 [rows,
+    2*inter] (bf16=True), the recomputed y BF16 [rows, inter] (want_y=True)
+    and the 1x128 quantization of dx (quantize=True; inter a multiple of 128).
+    """
+    torch = _torch()
+    if x_scales is None:
+        _need(x, torch.bfloat16, "x")
+    else:
+        _need(x, torch.uint8, "x")
+        _contig_f32(x_scales, "x_scales")
+    _need(dy, torch.bfloat16, "dy")
+    _row_major(x, "x")
+    _row_major(dy, "dy")
+    rows, two_inter = x.shape
+    if two_inter % 2:
+        raise ValueError("x must have an even number of columns (gate | up)")
+    inter = two_inter // 2
+    if tuple(dy.shape) != (rows, inter):
+        raise ValueError(f"dy must be [{rows}, {inter}], got {tuple(dy.shape)}")
+    if x_scales is not None and tuple(x_scales.shape) != (rows, two_inter // 128):
+        raise ValueError(f"x_scales must be [{rows}, {two_inter // 128}], got {tuple(x_scales.shape)}")
+    if inter % 128 and (x_scales is not None or quantize):
+        raise ValueError("inter must be a multiple of 128 for the FP8 cache and for a quantized dx")
+    if not (bf16 or quantize or want_y):
+        raise ValueError("nothing to compute: ask for bf16, quantize or want_y")
+    dev = _one_device(x, dy, x_scales)
+    dx = torch.empty((rows, two_inter), dtype=torch.bfloat16, device=dev) if bf16 else None
+    y = torch.empty((rows, inter), dtype=torch.bfloat16, device=dev) if want_y else None
+    codes = scales = None
+    if quantize:
+        codes = _alloc_codes(rows, two_inter, dev)
+        scales = torch.empty((rows, two_inter // 128), dtype=torch.float32, device=dev)
+    _call(dev, "fp8q_swiglu_backward", _addr(x), _addr(x_scales), rows, inter, _ld(x, two_inter), _addr(dy),
+          _ld(dy, inter), _addr(dx), _ld(dx, two_inter), _scale_mode(scale_mode), _addr(codes), _ld(codes, two_inter),
+          _addr(scales), _addr(y), _ld(y, inter))
+    return dx, y, codes, scales
+
+
+def grouped_wgrad(dy_t, dy_scales, x_t, x_scales, offsets, out=None, acc="fp32"):
+    """dW[g] = dY_g^T X_g (float32 [G, Nout, Kin]) over each group's rows of
+    the sorted token axis, from token-axis-quantized operands [Nout, rows_cap]
+    and [Kin, rows_cap].
+
+    offsets: int32 device tensor [G+1] of multiples of 128 (``moe_sort`` with
+    align=128).  An empty group gives zeros.
+    """
+    torch = _torch()
+    _contig_codes(dy_t, "dy_t")
+    _contig_codes(x_t, "x_t")
+    _contig_f32(dy_scales, "dy_scales")
+    _contig_f32(x_scales, "x_scales")
+    _need(offsets, torch.int32, "offsets")
+    if offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 [G+1] tensor")
+    if dy_t.dim() != 2 or x_t.dim() != 2 or dy_t.shape[1] != x_t.shape[1]:
+        raise ValueError("operand shapes do not match")
+    nout, cap = dy_t.shape
+    kin = x_t.shape[0]
+    if cap % 128:
+        raise ValueError("the token axis must be a multiple of 128")
+    if tuple(dy_scales.shape) != (nout, cap // 128) or tuple(x_scales.shape) != (kin, cap // 128):
+        raise ValueError("scales must be [rows of the codes, tokens/128]")
+    g = offsets.numel() - 1
+    if out is None:
+        dw = torch.empty((g, nout, kin), dtype=torch.float32, device=dy_t.device)
+    else:
+        dw = out
+        _need(dw, torch.float32, "out")
+        if tuple(dw.shape) != (g, nout, kin):
+            raise ValueError(f"out must be [{g}, {nout}, {kin}], got {tuple(dw.shape)}")
+        if dw.numel() and (dw.stride(2) != 1 or dw.stride(1) < kin or (g > 1 and dw.stride(0) != nout * dw.stride(1))):
+            raise ValueError("out must have contiguous rows and matrices that follow one another")
+    dev = _one_device(dy_t, dy_scales, x_t, x_scales, offsets, dw)
+    args = (_addr(dy_t), _addr(dy_scales), _addr(x_t), _addr(x_scales), _addr(offsets), g, cap, nout, kin)
+    tail = (_addr(dw), dw.stride(1) if dw.numel() else max(kin, 1))
+    code = _acc_code(acc)
+    if code == ACC_FP32:
+        _call(dev, "fp8q_grouped_wgrad", *args, *tail)
+    else:
+        _call(dev, "fp8q_grouped_wgrad_ex", *args, code, *tail)
+    return dw

@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +22,8 @@ LIB = os.path.join(PKG, "libfp8q.so")
 # the bench's plain streaming kernel (a measuring stick, not part of libfp8q)
 STREAMREF_LIB = os.path.join(PKG, "libfp8q_streamref.so")
 
-SOURCES = ["quant.hip", "gemm.hip", "gemm_small.hip", "moe.hip", "fp8q_api.cpp"]
+SOURCES = ["quant.hip", "gemm.hip", "gemm_small.hip", "moe.hip", "moe_route.hip", "moe_swiglu_bwd.hip", "fp8q_api.cpp",
+           "fp8q_moe_api.cpp"]
 
 # -ffp-contract=off: every fused multiply-add in the kernels is written out
 # explicitly (the quotient correction and the scale fold depend on it).
@@ -58,11 +60,10 @@ def _run(cmd, verbose):
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        _run([cc, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
-        objs.append(obj)
+    objs = [os.path.join(BUILD, src + ".o") for src in SOURCES]
+    with ThreadPoolExecutor(4) as pool:  # one compiler process per source
+        list(pool.map(lambda so: _run([cc, *COMMON, "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
+                      zip(SOURCES, objs)))
     tmp = LIB + ".tmp"
     # --no-undefined: a kernel whose host launch stub the compiler failed to
     # emit shows up here instead of when the library is loaded

@@ -78,4 +78,34 @@ hipError_t launch_swiglu_quant(const uint16_t* x, int rows, int inter, int64_t l
                                int64_t ldc, float* scales, bool cache_pow2, uint8_t* ccodes, int64_t ldcc,
                                float* cscales, hipStream_t stream);
 
+// Routing table (moe_route.hip): one workgroup alone up to
+// kSortPairsPerBlock pairs; above, at most kMaxSortBlocks of them, after a
+// launch that counts each one's share (hist: int32 [blocks, groups]).
+constexpr int kMaxSortGroups = 512;
+constexpr int kSortPairsPerBlock = 4096;
+constexpr int kMaxSortBlocks = 256;
+inline int sort_blocks(int pairs) {
+  const int want = (int)(((int64_t)pairs + kSortPairsPerBlock - 1) / kSortPairsPerBlock);
+  return want < 1 ? 1 : want < kMaxSortBlocks ? want : kMaxSortBlocks;
+}
+hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, int64_t ld, int64_t first, int groups,
+                           int align, int cap, int* offsets, int* token, int* row_of, int* hist, hipStream_t stream);
+hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t ldy, const int* row_of,
+                              const float* weights, int tokens, int topk, bool out_f32, void* out, int64_t ldo,
+                              hipStream_t stream);
+// y == nullptr: no weight gradient; dy / codes == nullptr: that form of the rows is not written
+hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int tokens, int n, int64_t lddo,
+                                       const void* y, bool y_f32, int cap, int64_t ldy, const int* row_of,
+                                       const float* weights, int topk, const int* token, uint16_t* dy, int64_t lddy,
+                                       bool pow2, uint8_t* codes, int64_t ldc, float* scales, float* dweights,
+                                       hipStream_t stream);
+// xscales == nullptr: x is BF16; else x are E4M3 codes with 1x128 scales
+hipError_t launch_swiglu_backward(const void* x, const float* xscales, int rows, int inter, int64_t ldx,
+                                  const uint16_t* dy, int64_t lddy, uint16_t* dx, int64_t lddx, bool pow2,
+                                  uint8_t* codes, int64_t ldc, float* scales, uint16_t* y, int64_t ldy,
+                                  hipStream_t stream);
+hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint8_t* x_t,
+                                const float* x_scales, const int32_t* offsets, int groups, int cap, int nout,
+                                int kin, int acc, float* dw, int64_t lddw, hipStream_t stream);
+
 }  // namespace fp8q

@@ -1,0 +1,460 @@
+// The way of tokens to the experts of one device and back (gfx950): the
+// routing table the dispatch gather and the grouped GEMMs read, the weighted
+// sum of a token's expert rows, and the gradient of that sum.
+//
+// * Sort: the (token, choice) pairs of the hosted experts, ordered by expert
+//   and inside an expert by pair index (a stable counting sort), with every
+//   expert's rows starting at a multiple of `align`.
+// * Combine: out[t] = sum_j w[t,j] y[row_of[t,j]], float32, one rounding.
+// * Combine backward: dy[row_of[t,j]] = bf16(w[t,j] dout[t]), optionally
+//   quantized per 1x128 tile (jp-study.kr doc 258368 ¶1, tmdrlife.com
+//   wr_id=13334 ¶4: the activation gradient before the down-projections is
+//   one of the tensors that take FP8), and dw[t,j] = <dout[t], y[row]>.
+#include "fp8q_internal.h"
+#include "quant_common.h"
+
+namespace fp8q {
+namespace {
+
+// ------------------------------------------------------------------ sort ---
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+
+struct SortArgs {
+  const void* experts;  // [tokens, ld] int32 or int64
+  int topk;
+  int64_t ld;
+  int64_t first;        // hosted experts: first .. first + groups - 1
+  int groups, align;
+  int pairs;            // tokens * topk
+  int cap;              // rows of the sorted layout
+  int chunk;            // pairs per workgroup, a multiple of kSortThreads
+  int* offsets;         // [groups + 1]
+  int* token;           // [cap]
+  int* row_of;          // [pairs]
+  int* hist;            // [workgroups, groups] pairs of each workgroup's chunk per expert (more than one workgroup)
+};
+
+// Hosted expert of pair p, -1 for an expert of another device.
+template <typename IDX>
+__device__ __forceinline__ int local_expert(const SortArgs& a, int p) {
+  const int t = (int)((unsigned)p / (unsigned)a.topk);
+  const int64_t e = (int64_t)static_cast<const IDX*>(a.experts)[(int64_t)t * a.ld + (p - t * a.topk)] - a.first;
+  return e >= 0 && e < a.groups ? (int)e : -1;
+}
+
+// Lanes of the wave that hold the same expert as this one (0 for e < 0):
+// one ballot per bit of the expert index.
+__device__ __forceinline__ uint64_t same_expert(int e, int bits) {
+  uint64_t mask = __builtin_amdgcn_ballot_w64(e >= 0);
+  for (int i = 0; i < bits; ++i) {
+    const uint64_t set = __builtin_amdgcn_ballot_w64((e >> i) & 1);
+    mask &= ((e >> i) & 1) ? set : ~set;
+  }
+  return e >= 0 ? mask : 0;
+}
+
+__device__ __forceinline__ int index_bits(int groups) { return groups > 1 ? 32 - __clz(groups - 1) : 0; }
+
+// Pairs per expert of each workgroup's chunk.
+template <typename IDX>
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+  __shared__ int cnt[kMaxSortGroups];
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int e = tid; e < a.groups; e += kSortThreads) cnt[e] = 0;
+  __syncthreads();
+  const int bits = index_bits(a.groups);
+  const int64_t p0 = (int64_t)blockIdx.x * a.chunk;
+  for (int i = 0; i < a.chunk; i += kSortThreads) {
+    const int64_t p = p0 + i + tid;
+    const int e = p < a.pairs ? local_expert<IDX>(a, (int)p) : -1;
+    const uint64_t same = same_expert(e, bits);
+    if (same && lane == __builtin_ctzll(same)) atomicAdd(&cnt[e], __builtin_popcountll(same));
+  }
+  __syncthreads();
+  for (int e = tid; e < a.groups; e += kSortThreads) a.hist[(int64_t)blockIdx.x * a.groups + e] = cnt[e];
+}
+
+// Every workgroup forms the whole table of group starts for itself (from the
+// per-chunk counts, or, alone, from its own) and places its chunk: wave w
+// takes the w-th sixteenth of it in order, so a pair's row is the group's
+// start + the pairs of that expert in earlier chunks, in earlier waves, in
+// earlier steps of this wave (a running count in LDS) and in lower lanes.
+template <typename IDX>
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
+  extern __shared__ int lds[];
+  const int G = a.groups;
+  int* cnt = lds;                      // [kSortWaves][G]: running counts
+  int* total = cnt + kSortWaves * G;   // [G] pairs of the expert
+  int* start = total + G;              // [G + 1] first row of the group
+  int* scan = start + G + 1;           // [kSortWaves]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int blk = blockIdx.x, blocks = gridDim.x;
+  for (int i = tid; i < (kSortWaves + 2) * G + 1; i += kSortThreads) lds[i] = 0;
+  __syncthreads();
+
+  const int bits = index_bits(G);
+  const int per_wave = a.chunk / kSortWaves;
+  const int64_t p0 = (int64_t)blk * a.chunk + (int64_t)wave * per_wave;
+  for (int i = 0; i < per_wave; i += 64) {
+    const int64_t p = p0 + i + lane;
+    const int e = p < a.pairs ? local_expert<IDX>(a, (int)p) : -1;
+    const uint64_t same = same_expert(e, bits);
+    if (same && lane == __builtin_ctzll(same)) atomicAdd(&cnt[wave * G + e], __builtin_popcountll(same));
+  }
+  // pairs of each expert in all chunks, and in the chunks before this one
+  // (kept in start[] until the group starts are known)
+  if (blocks > 1) {
+    for (int i = tid; i < blocks * G; i += kSortThreads) {
+      const int b = i / G, e = i - b * G;
+      const int h = a.hist[i];
+      if (h) {
+        atomicAdd(&total[e], h);
+        if (b < blk) atomicAdd(&start[e], h);
+      }
+    }
+  }
+  __syncthreads();
+  // exclusive running counts: before this wave (and, for wave 0, before this chunk)
+  int mine = 0, padded = 0;
+  if (tid < G) {
+    int run = start[tid];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = cnt[w * G + tid];
+      cnt[w * G + tid] = run;
+      run += c;
+    }
+    mine = blocks > 1 ? total[tid] : run;
+    padded = (int)(((int64_t)mine + a.align - 1) / a.align * a.align);
+  }
+  // inclusive scan of the padded group sizes (G <= kSortThreads)
+  int inc = padded;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(inc, d);
+    if (lane >= d) inc += v;
+  }
+  if (lane == 63) scan[wave] = inc;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) inc += scan[w];
+  if (tid < G) {
+    total[tid] = mine;
+    start[tid] = inc - padded;
+    if (tid == G - 1) start[G] = inc;
+  }
+  __syncthreads();
+  if (blk == 0)
+    for (int g = tid; g <= G; g += kSortThreads) a.offsets[g] = min(start[g], a.cap);
+
+  for (int i = 0; i < per_wave; i += 64) {
+    const int64_t p = p0 + i + lane;
+    const int e = p < a.pairs ? local_expert<IDX>(a, (int)p) : -1;
+    const uint64_t same = same_expert(e, bits);
+    const int first = same ? __builtin_ctzll(same) : 0;
+    int before = 0;
+    if (same && lane == first) before = atomicAdd(&cnt[wave * G + e], __builtin_popcountll(same));
+    before = __shfl(before, first);
+    if (p < a.pairs) {
+      int row = -1;
+      if (e >= 0) {
+        row = start[e] + before + __builtin_popcountll(same & ((uint64_t(1) << lane) - 1));
+        if (row < a.cap) {
+          a.token[row] = (int)((unsigned)p / (unsigned)a.topk);
+        } else {
+          row = -1;
+        }
+      }
+      a.row_of[p] = row;
+    }
+  }
+  // rows without a pair: the padding of every group, and everything behind
+  // the last one
+  if (a.align > 1) {
+    for (int g = blk; g < G; g += blocks) {
+      const int end = min(start[g + 1], a.cap);
+      for (int r = start[g] + total[g] + tid; r < end; r += kSortThreads) a.token[r] = -1;
+    }
+  }
+  for (int64_t r = (int64_t)start[G] + blk * kSortThreads + tid; r < a.cap; r += (int64_t)blocks * kSortThreads)
+    a.token[r] = -1;
+}
+
+// ------------------------------------------------------- 8-element chunks ---
+struct F8 {
+  float v[8];
+};
+
+template <bool F32>
+__device__ __forceinline__ F8 load8(const void* base, int64_t at, int nvalid, bool vec) {
+  F8 r;
+  if constexpr (F32) {
+    const float* p = static_cast<const float*>(base) + at;
+    if (vec) {
+      const uint4 a = ld_stream16(p), b = ld_stream16(p + 4);
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.v[i] = i < nvalid ? p[i] : 0.0f;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    const uint4 a = vec ? ld_stream16(p) : load8_masked(p, nvalid);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.v[2 * i] = bf16_lo(w[i]);
+      r.v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  return r;
+}
+
+// Eight float32 values -> BF16 in chunk layout, nearest even by the hardware
+// convert (infinities and NaN stay what they are).
+typedef __bf16 mr_v2bf __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint4 pack8_bf16(const F8& f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(uint32_t, mr_v2bf{(__bf16)f.v[2 * i], (__bf16)f.v[2 * i + 1]});
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store8_bf16(uint16_t* p, uint4 c, int nvalid, bool vec) {
+  if (vec) {
+    st_stream16(p, c);
+    return;
+  }
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < nvalid) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+}
+
+__device__ __forceinline__ void store8_f32(float* p, const F8& f, int nvalid, bool vec) {
+  if (vec) {
+    st_stream16(p, make_uint4(__float_as_uint(f.v[0]), __float_as_uint(f.v[1]), __float_as_uint(f.v[2]), __float_as_uint(f.v[3])));
+    st_stream16(p + 4, make_uint4(__float_as_uint(f.v[4]), __float_as_uint(f.v[5]), __float_as_uint(f.v[6]), __float_as_uint(f.v[7])));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < nvalid) p[i] = f.v[i];
+}
+
+// --------------------------------------------------------------- combine ---
+// One workgroup per token and chunk of 8 x threads columns: the rows and
+// weights of the token are wave-uniform, and the chunks of up to eight rows
+// are in flight at once.
+template <bool YF32, bool OF32>
+__global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y, int cap, int n, int64_t ldy,
+                               const int* __restrict__ row_of, const float* __restrict__ weights, int topk,
+                               int chunks, void* __restrict__ out, int64_t ldo, bool vec) {
+  const int t = blockIdx.x / chunks;
+  const int col = ((blockIdx.x - t * chunks) * (int)blockDim.x + (int)threadIdx.x) * 8;
+  if (col >= n) return;
+  const int* rows = row_of + (int64_t)t * topk;
+  const float* w = weights ? weights + (int64_t)t * topk : nullptr;
+  F8 acc;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc.v[i] = 0.0f;
+  for (int j0 = 0; j0 < topk; j0 += 8) {
+    F8 v[8];
+    bool has[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int r = j0 + u < topk ? rows[j0 + u] : -1;
+      has[u] = (unsigned)r < (unsigned)cap;
+      if (has[u]) v[u] = load8<YF32>(y, (int64_t)r * ldy + col, n - col, vec);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (!has[u]) continue;
+      const float wj = w ? w[j0 + u] : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc.v[i] = __builtin_fmaf(wj, v[u].v[i], acc.v[i]);
+    }
+  }
+  if constexpr (OF32) {
+    store8_f32(static_cast<float*>(out) + (int64_t)t * ldo + col, acc, n - col, vec);
+  } else {
+    store8_bf16(static_cast<uint16_t*>(out) + (int64_t)t * ldo + col, pack8_bf16(acc), n - col, vec);
+  }
+}
+
+// ------------------------------------------------------ combine backward ---
+struct CombineBwdArgs {
+  const void* dout;
+  int64_t lddo;
+  const void* y;         // null: no weight gradient
+  int64_t ldy;
+  const int* row_of;
+  const float* weights;  // null: 1
+  const int* token;      // null: rows without a pair are left alone
+  uint16_t* dy;          // null: no BF16 rows
+  int64_t lddy;
+  uint8_t* codes;        // null: no E4M3 rows
+  int64_t ldc;
+  float* scales;
+  float* dweights;
+  int pairs, topk, n, cap;
+  bool vec;
+};
+
+constexpr int kZeroRows = 64;  // rows looked over by one of the trailing workgroups
+
+// Workgroup p < pairs: pair p.  The pairs of a token follow one another on
+// one XCD, so its gradient row comes from HBM once and from that XCD's L2
+// for the other choices.  The workgroups behind the pairs clear the rows
+// without a pair.
+template <bool DF32, bool YF32, bool POW2>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
+  __shared__ float part[4];
+  const int tid = threadIdx.x;
+  const int nb = (a.n + 127) >> 7;
+  if ((int)blockIdx.x >= a.pairs) {
+    const int r0 = ((int)blockIdx.x - a.pairs) * kZeroRows;
+    for (int r = r0; r < min(r0 + kZeroRows, a.cap); ++r) {
+      if (a.token[r] >= 0) continue;
+      for (int col = tid * 8; col < a.n; col += 2048) {
+        if (a.dy) store8_bf16(a.dy + (int64_t)r * a.lddy + col, make_uint4(0, 0, 0, 0), a.n - col, a.vec);
+        if (a.codes) {
+          uint8_t* dst = a.codes + (int64_t)r * a.ldc + col;
+          if (a.vec) {
+            st_stream8(dst, make_uint2(0, 0));
+          } else {
+            store8_masked(dst, make_uint2(0, 0), a.n - col);
+          }
+        }
+      }
+      if (a.codes)
+        for (int j = tid; j < nb; j += 256) a.scales[(int64_t)r * nb + j] = 0.0f;
+    }
+    return;
+  }
+  // contiguous pairs on one XCD (workgroup i runs on XCD i % 8)
+  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+  const int per = a.pairs >> 3, rem = a.pairs & 7;
+  const int p = xcd * per + min(xcd, rem) + idx;
+  const int row = a.row_of[p];
+  if ((unsigned)row >= (unsigned)a.cap) {
+    if (tid == 0 && a.dweights) a.dweights[p] = 0.0f;
+    return;
+  }
+  const int t = (int)((unsigned)p / (unsigned)a.topk);
+  const float w = a.weights ? a.weights[p] : 1.0f;
+  float dot = 0.0f;
+  for (int c0 = 0; c0 < a.n; c0 += 2048) {
+    const int col = c0 + tid * 8, left = a.n - col;
+    F8 g, v;
+    const bool in = left > 0;
+    if (in) {
+      g = load8<DF32>(a.dout, (int64_t)t * a.lddo + col, left, a.vec);
+      if (a.y) v = load8<YF32>(a.y, (int64_t)row * a.ldy + col, left, a.vec);
+    }
+    if (in && a.y) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(g.v[i], v.v[i], dot);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g.v[i] = in ? w * g.v[i] : 0.0f;
+    const uint4 d = pack8_bf16(g);
+    if (a.dy && in) store8_bf16(a.dy + (int64_t)row * a.lddy + col, d, left, a.vec);
+    if (a.codes) {
+      // a 16-lane DPP row holds one 1x128 tile; every lane takes part
+      const TileScale ts = tile_scale<POW2>(dpp_max16(absmax8(d)));
+      const uint2 c = encode8<POW2>(d, ts);
+      if (in) {
+        uint8_t* dst = a.codes + (int64_t)row * a.ldc + col;
+        if (a.vec) {
+          st_stream8(dst, c);
+        } else {
+          store8_masked(dst, c, left);
+        }
+        if ((tid & 15) == 0) a.scales[(int64_t)row * nb + (col >> 7)] = ts.s;
+      }
+    }
+  }
+  if (!a.dweights) return;
+  for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
+  if ((tid & 63) == 0) part[tid >> 6] = dot;
+  __syncthreads();
+  if (tid == 0) a.dweights[p] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+}  // namespace
+
+template <typename IDX>
+static hipError_t launch_sort(SortArgs a, int blocks, hipStream_t stream) {
+  if (blocks > 1) hipLaunchKernelGGL(sort_count_kernel<IDX>, dim3(blocks), dim3(kSortThreads), 0, stream, a);
+  const size_t lds = ((size_t)(kSortWaves + 2) * a.groups + 1 + kSortWaves) * sizeof(int);
+  hipLaunchKernelGGL(sort_place_kernel<IDX>, dim3(blocks), dim3(kSortThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, int64_t ld, int64_t first, int groups,
+                           int align, int cap, int* offsets, int* token, int* row_of, int* hist,
+                           hipStream_t stream) {
+  SortArgs a{};
+  a.experts = experts; a.topk = topk; a.ld = ld; a.first = first; a.groups = groups; a.align = align;
+  a.pairs = pairs; a.cap = cap; a.offsets = offsets; a.token = token; a.row_of = row_of; a.hist = hist;
+  const int blocks = sort_blocks(pairs);
+  const int64_t per = ((int64_t)pairs + blocks - 1) / blocks;
+  a.chunk = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
+  if (a.chunk == 0) a.chunk = kSortThreads;
+  return i64 ? launch_sort<int64_t>(a, blocks, stream) : launch_sort<int32_t>(a, blocks, stream);
+}
+
+hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t ldy, const int* row_of,
+                              const float* weights, int tokens, int topk, bool out_f32, void* out, int64_t ldo,
+                              hipStream_t stream) {
+  const bool vec = n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0;
+  // workgroups of 256, 128 or 64 threads, whichever leaves the fewest idle
+  const int items = (n + 7) / 8;
+  int threads = 256;
+  for (int c = 128; c >= 64; c >>= 1)
+    if ((items + c - 1) / c * c < (items + threads - 1) / threads * threads) threads = c;
+  const int chunks = (items + threads - 1) / threads;
+  const dim3 grid((unsigned)(tokens * chunks)), block(threads);
+  if (y_f32) {
+    if (out_f32)
+      hipLaunchKernelGGL((combine_kernel<true, true>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
+    else
+      hipLaunchKernelGGL((combine_kernel<true, false>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
+  } else {
+    if (out_f32)
+      hipLaunchKernelGGL((combine_kernel<false, true>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
+    else
+      hipLaunchKernelGGL((combine_kernel<false, false>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
+  }
+  return hipGetLastError();
+}
+
+template <bool DF32, bool YF32>
+static void launch_bwd(const CombineBwdArgs& a, int grid, bool pow2, hipStream_t stream) {
+  if (pow2)
+    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, true>), dim3(grid), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, false>), dim3(grid), dim3(256), 0, stream, a);
+}
+
+hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int tokens, int n, int64_t lddo,
+                                       const void* y, bool y_f32, int cap, int64_t ldy, const int* row_of,
+                                       const float* weights, int topk, const int* token, uint16_t* dy,
+                                       int64_t lddy, bool pow2, uint8_t* codes, int64_t ldc, float* scales,
+                                       float* dweights, hipStream_t stream) {
+  CombineBwdArgs a{};
+  a.dout = dout; a.lddo = lddo; a.y = y; a.ldy = ldy; a.row_of = row_of; a.weights = weights; a.token = token;
+  a.dy = dy; a.lddy = lddy; a.codes = codes; a.ldc = ldc; a.scales = scales; a.dweights = dweights;
+  a.pairs = tokens * topk; a.topk = topk; a.n = n; a.cap = cap;
+  a.vec = n % 8 == 0 && lddo % 8 == 0 && (!y || ldy % 8 == 0) && (!dy || lddy % 8 == 0) && (!codes || ldc % 8 == 0);
+  const int zero = token && (dy || codes) ? (cap + kZeroRows - 1) / kZeroRows : 0;
+  const int grid = a.pairs + zero;
+  if (dout_f32) {
+    y_f32 ? launch_bwd<true, true>(a, grid, pow2, stream) : launch_bwd<true, false>(a, grid, pow2, stream);
+  } else {
+    y_f32 ? launch_bwd<false, true>(a, grid, pow2, stream) : launch_bwd<false, false>(a, grid, pow2, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace fp8q

@@ -27,8 +27,8 @@
  *    128-token x 1-feature tiles.
  *
  * Conventions for every call:
- *  - Memory: all pointers are DEVICE pointers owned by the caller.  The
- *    library allocates nothing, frees nothing and keeps no pointer after
+ *  - Memory: all pointers are DEVICE pointers owned by the caller, scratch
+ *    memory (workspace) included.  The library allocates nothing, frees nothing and keeps no pointer after
  *    the call returns.
  *  - Execution: work is enqueued on `stream` (0 = the null stream) and the
  *    call returns without synchronizing.  There is no global mutable state
@@ -108,6 +108,7 @@ enum { FP8Q_OUT_F32 = 0, FP8Q_OUT_BF16 = 1 };
  *    two quantization of BF16 values with max-abs >= 2^-92 gives); scales
  *    that are not powers of two give wrong results. */
 enum { FP8Q_ACC_FP32 = 0, FP8Q_ACC_FP8_MFMA = 1, FP8Q_ACC_FP8_MFMA_SCALED = 2, FP8Q_ACC_FP32_POW2 = 3 };
+enum { FP8Q_INDEX_I32 = 0, FP8Q_INDEX_I64 = 1 };
 enum {
   FP8Q_TILE_ROW = 0,    /* 1x128 tiles along cols: codes [rows, ld_codes], scales [rows, ceil(cols/128)] */
   FP8Q_TILE_TOKEN_T = 1 /* 128x1 tiles along rows (the token axis), codes written transposed:
@@ -324,6 +325,134 @@ fp8q_status fp8q_swiglu_quantize(const void* x_bf16, int64_t rows, int64_t inter
                                  int scale_mode, uint8_t* codes, int64_t ld_codes, float* scales,
                                  int cache_scale_mode, uint8_t* cache_codes, int64_t ld_cache,
                                  float* cache_scales, hipStream_t stream);
+
+/* ---- the expert (MoE) layer around the GEMMs --------------------------------
+ * Forward: fp8q_quantize_act, fp8q_moe_sort, fp8q_gather_rows (its index is
+ * `token`), fp8q_grouped_gemm, fp8q_swiglu_quantize, fp8q_grouped_gemm,
+ * fp8q_moe_combine.  Backward: fp8q_moe_combine_backward, fp8q_grouped_gemm
+ * with transposed weights, fp8q_swiglu_backward, fp8q_grouped_gemm,
+ * fp8q_moe_combine without weights (the dispatch's gradient) and
+ * fp8q_grouped_wgrad per projection. */
+
+/* Routing table of the experts first_expert .. first_expert + G - 1 that one
+ * device hosts (jp-study.kr doc 258368 ¶1-¶2: 256 routed experts, eight per
+ * token, several hosted per device).
+ * experts: DEVICE int32 or int64 (index_dtype FP8Q_INDEX_I32 / _I64)
+ * [tokens, ld_experts >= topk], the expert of every (token, choice) pair;
+ * pairs of experts hosted elsewhere (any other value) get no row.  The rows
+ * of the sorted layout are the hosted pairs ordered by expert and, within an
+ * expert, by t * topk + j (a stable sort; the result does not depend on
+ * scheduling); an expert chosen twice by one token gets two rows.  Every
+ * expert's rows start at a multiple of align (1, or 128 for
+ * fp8q_grouped_wgrad, whose tiles are 128 tokens long):
+ *   offsets int32[G+1]: group g is rows [offsets[g], offsets[g+1]), padding
+ *     included;
+ *   token int32[rows_cap]: the token of each row, -1 for padding and for all
+ *     rows from offsets[G] on (fp8q_gather_rows writes zero rows for -1);
+ *   row_of int32[tokens, topk]: the row of each pair, -1 without one.
+ * rows_cap is a multiple of align.  Pairs whose row would be rows_cap or more
+ * are dropped (row -1) and offsets stop at rows_cap; rows_cap >= tokens *
+ * topk + G * (align - 1), rounded up to align, drops none.
+ * workspace: DEVICE memory of at least fp8q_moe_sort_workspace(tokens, topk,
+ * G) bytes (0 for a few thousand pairs: then it may be NULL), used until the
+ * call's work is done; calls that may run at the same time need one each.
+ * A missing or small workspace gives FP8Q_ERR_INVALID_ARG.  G <= 512 and
+ * tokens * topk + G * align < 2^31, else FP8Q_ERR_SHAPE. */
+int64_t fp8q_moe_sort_workspace(int64_t tokens, int64_t topk, int32_t G);
+fp8q_status fp8q_moe_sort(const void* experts, int index_dtype, int64_t tokens, int64_t topk, int64_t ld_experts,
+                          int64_t first_expert, int32_t G, int32_t align, int64_t rows_cap,
+                          int32_t* offsets, int32_t* token, int32_t* row_of,
+                          void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Weighted sum of each token's expert rows (gnrental.net wr_id=40936: the
+ * combine stays in BF16):
+ *   out[t, n] = sum_j weights[t, j] * y[row_of[t, j], n]
+ * over j = 0 .. topk-1 in that order, in float32 with fused multiply-adds,
+ * rounded once (nearest even) for a BF16 out.  Pairs whose row lies outside
+ * [0, rows_cap) add nothing (their weight is not used); a token without any
+ * gets zeros.  y [rows_cap, ld_y >= N] and out [tokens, ld_out >= N] are
+ * FP8Q_OUT_F32 or FP8Q_OUT_BF16 (y_dtype, out_dtype); weights float32
+ * [tokens, topk], or NULL for the plain sum, which is also the gradient of
+ * fp8q_gather_rows' row copy: dX[t] = sum over the rows of t.  Non-finite
+ * values of y follow float32 arithmetic; rows no pair names are not read.
+ * tokens * ceil(N/512) < 2^24, else FP8Q_ERR_SHAPE. */
+fp8q_status fp8q_moe_combine(const void* y, int y_dtype, int64_t rows_cap, int64_t N, int64_t ld_y,
+                             const int32_t* row_of, const float* weights, int64_t tokens, int64_t topk,
+                             int out_dtype, void* out, int64_t ld_out, hipStream_t stream);
+
+/* Gradient of fp8q_moe_combine for dout [tokens, ld_dout >= N] (dout_dtype):
+ *   dy[row_of[t, j], n] = bf16_rne(weights[t, j] * dout[t, n])
+ *   dweights[t, j] = sum_n dout[t, n] * y[row_of[t, j], n]   (float32)
+ * dy is written as BF16 (dy_bf16 [rows_cap, ld_dy >= N]) and / or quantized
+ * per 1x128 tile along N exactly as fp8q_quantize_act(FP8Q_TILE_ROW,
+ * scale_mode) quantizes that BF16 tensor (dy_codes [rows_cap, ld_codes >= N],
+ * dy_scales [rows_cap, ceil(N/128)]; tmdrlife.com wr_id=13334 ¶4: the
+ * activation gradient before the down-projections takes power-of-two
+ * scales); dy_bf16, dy_codes and dweights may each be NULL (then that output
+ * is not formed; y is read only for dweights and may be NULL without it).
+ * weights NULL means 1 everywhere.  Pairs without a row in [0, rows_cap) get
+ * dweights 0.  token [rows_cap] is fp8q_moe_sort's: rows whose token is
+ * negative (padding and everything behind the last group) are written as
+ * zero values, codes and scales; with token NULL rows that no pair names are
+ * left as they were.  No two pairs may name the same row.  For the quantized
+ * form every product must be a finite BF16 value.
+ * tokens * topk + rows_cap/64 < 2^24 - 1, else FP8Q_ERR_SHAPE. */
+fp8q_status fp8q_moe_combine_backward(const void* dout, int dout_dtype, int64_t tokens, int64_t N, int64_t ld_dout,
+                                      const void* y, int y_dtype, int64_t rows_cap, int64_t ld_y,
+                                      const int32_t* row_of, const float* weights, int64_t topk,
+                                      const int32_t* token, void* dy_bf16, int64_t ld_dy, int scale_mode,
+                                      uint8_t* dy_codes, int64_t ld_codes, float* dy_scales, float* dweights,
+                                      hipStream_t stream);
+
+/* Gradient of the SwiGLU of fp8q_swiglu_quantize (tmdrlife.com wr_id=13334
+ * ¶4: the inputs are cached in FP8 and the output recomputed in the backward
+ * pass).  x = [gate | up] is BF16 [rows, ld_x >= 2*inter] (x_scales NULL) or
+ * the FP8 cache that fp8q_swiglu_quantize writes (E4M3 codes [rows, ld_x],
+ * x_scales [rows, 2*inter/128], inter a multiple of 128; x = code * scale).
+ * With g, u the two halves, s = 1 / (1 + exp(-g)) and dy BF16
+ * [rows, ld_dy >= inter], in float32, each output rounded once to BF16:
+ *   dx[:, 0:inter]       = dy * u * s * (1 + g * (1 - s))
+ *   dx[:, inter:2*inter] = dy * g * s
+ *   y                    = g * s * u
+ * dx_bf16 [rows, ld_dx >= 2*inter], the 1x128 quantization of that BF16
+ * tensor (dx_codes [rows, ld_codes >= 2*inter], dx_scales
+ * [rows, 2*inter/128], scale_mode; inter a multiple of 128) and y_bf16
+ * [rows, ld_y >= inter] (for the down-projection's weight gradient) are each
+ * written where the pointer is not NULL; one at least must be given.  Inputs
+ * must be finite, and every dy * u and every output below the largest finite
+ * float32 and BF16 value. */
+fp8q_status fp8q_swiglu_backward(const void* x, const float* x_scales, int64_t rows, int64_t inter, int64_t ld_x,
+                                 const void* dy_bf16, int64_t ld_dy, void* dx_bf16, int64_t ld_dx,
+                                 int scale_mode, uint8_t* dx_codes, int64_t ld_codes, float* dx_scales,
+                                 void* y_bf16, int64_t ld_y, hipStream_t stream);
+
+/* FP8 weight gradients of the experts one device hosts (jp-study.kr doc
+ * 258368 ¶3: Wgrad runs in FP8): fp8q_wgrad for every group of a sorted
+ * token axis,
+ *   dW[g, n, c] = sum_{b in group g} dy_scales[n,b] * x_scales[c,b] * sum_{t in block b} dY[t,n] * X[t,c]
+ * dy_t codes [Nout, rows_cap], dy_scales [Nout, rows_cap/128], x_t codes
+ * [Kin, rows_cap], x_scales [Kin, rows_cap/128]: FP8Q_TILE_TOKEN_T outputs of
+ * [rows_cap, .] tensors with ld_codes = rows_cap, a multiple of 128.  offsets:
+ * DEVICE int32[G+1], non-decreasing multiples of 128 in [0, rows_cap]
+ * (fp8q_moe_sort with align 128; its padding rows are zero after
+ * fp8q_gather_rows and fp8q_moe_combine_backward).  That is a precondition
+ * the kernel does not report: it clamps offsets to [0, rows_cap] and rounds
+ * them down to 128, so a broken table gives wrong gradients but no access
+ * outside the operands.  An empty group writes zeros.  dw float32
+ * [G, Nout, ld_dw >= Kin], overwritten.  Partials at float32 grade.  Each
+ * code operand is below 2 GiB, and G * ceil(Nout/256) * ceil(Kin/224) <
+ * 2^23, else FP8Q_ERR_SHAPE. */
+fp8q_status fp8q_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales,
+                               const uint8_t* x_t, const float* x_scales,
+                               const int32_t* offsets, int32_t G, int64_t rows_cap,
+                               int64_t Nout, int64_t Kin, float* dw, int64_t ld_dw, hipStream_t stream);
+
+/* fp8q_grouped_wgrad with the accumulation form acc (FP8Q_ACC_*), as
+ * fp8q_wgrad_ex extends fp8q_wgrad. */
+fp8q_status fp8q_grouped_wgrad_ex(const uint8_t* dy_t, const float* dy_scales,
+                                  const uint8_t* x_t, const float* x_scales,
+                                  const int32_t* offsets, int32_t G, int64_t rows_cap,
+                                  int64_t Nout, int64_t Kin, int acc, float* dw, int64_t ld_dw, hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* fp8q_status_string(fp8q_status s);
