@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libfp8q.so")
 # the bench's plain streaming kernel (a measuring stick, not part of libfp8q)
 STREAMREF_LIB = os.path.join(PKG, "libfp8q_streamref.so")
 
-SOURCES = ["quant.hip", "gemm.hip", "gemm_small.hip", "moe.hip", "moe_route.hip", "moe_swiglu_bwd.hip", "fp8q_api.cpp",
+SOURCES = ["quant.hip", "gemm.hip", "gemm_small.hip", "moe.hip", "moe_route.hip", "moe_swiglu_bwd.hip", "wgrad_grouped.hip", "fp8q_api.cpp",
            "fp8q_moe_api.cpp"]
 
 # -ffp-contract=off: every fused multiply-add in the kernels is written out

@@ -129,10 +129,10 @@ fp8q_status fp8q_grouped_wgrad_ex(const uint8_t* dy_t, const float* dy_scales, c
   if (G == 0 || Nout == 0 || Kin == 0) return FP8Q_OK;
   if (!offsets) return FP8Q_ERR_INVALID_ARG;
   if (fp8q_status st = check_gemm_common(rows_cap, FP8Q_OUT_F32, dw, ld_dw, Kin)) return st;
-  // tiles of 224 or 256 columns: bound the count with the narrower width
-  const int64_t tiles = tiles256(Nout, Kin, 224);
-  if (Nout * rows_cap >= kMaxOperandBytes || Kin * rows_cap >= kMaxOperandBytes || tiles >= kMaxGemmTiles ||
-      tiles * G >= kMaxGemmTiles)
+  // one workgroup of 256 threads per 128 x 128 outputs
+  const int64_t tiles = ((Nout + 127) / 128) * ((Kin + 127) / 128);
+  if (Nout * rows_cap >= kMaxOperandBytes || Kin * rows_cap >= kMaxOperandBytes || tiles >= kMaxGroups ||
+      tiles * G >= kMaxGroups)
     return FP8Q_ERR_SHAPE;
   if (rows_cap > 0) {
     if (!dy_t || !dy_scales || !x_t || !x_scales) return FP8Q_ERR_INVALID_ARG;

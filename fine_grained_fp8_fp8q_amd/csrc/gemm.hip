@@ -84,9 +84,7 @@ constexpr int kSmallStage = StageLayout<128>::kBytes;   // 48 KiB (also holds th
 constexpr int kSclHalf = (BM + BN) * 4 * 4;             // 8 KiB
 constexpr int kSclBytes = 2 * kSclHalf;
 
-// kGroupedWgrad: the weight gradient of every expert of one device, each over
-// its own range of the token axis.
-enum Mode { kDense = 0, kGrouped = 1, kWgrad = 2, kGroupedWgrad = 3 };
+enum Mode { kDense = 0, kGrouped = 1, kWgrad = 2 };
 // Output forms: float32, BF16 (RNE), or the BF16 value quantized per 1x128
 // tile along N to E4M3 codes plus float32 scales (free or power-of-two).
 enum Out { kOutF32 = 0, kOutBF16 = 1, kOutE4M3 = 2, kOutE4M3Pow2 = 3 };
@@ -104,8 +102,8 @@ struct GemmArgs {
   int64_t ldc;
   float* cs;              // quantized output: scales [rows, ceil(n/128)]
   bool vec_c;             // ldc % 4 == 0: 16-byte (f32) / 8-byte (bf16) row-fragment stores
-  int rows;               // dense: M; grouped: rows_cap; wgrad (grouped or not): Nout
-  int n, k, groups;       // grouped wgrad: k = rows_cap, offsets in multiples of 128 along it
+  int rows;               // dense: M; grouped: rows_cap; wgrad: Nout
+  int n, k, groups;
   int tiles_m, tiles_n;
   int bn;                 // tile width in N: 256, or 224 for the weight gradient (see launch_wgrad)
 };
@@ -142,8 +140,6 @@ struct Tile {
   int wrows;     // waves along M: 4 (256-row tile), 2 or 1 (tiles of at most 128 / 64 rows)
   const uint8_t* w;
   const float* sw;
-  int kb0, nkb;  // K blocks [kb0, kb0 + nkb)
-  int64_t c0;    // first element of the tile's output matrix
 };
 
 // XCD-aware order: workgroup i runs on XCD i % 8, so consecutive logical
@@ -158,35 +154,7 @@ __device__ __forceinline__ int xcd_logical(int bid, int nblk) {
 template <int MODE>
 __device__ __forceinline__ bool decode_tile(const GemmArgs& g, Tile& t) {
   const int nkb = g.k / BK;
-  t.kb0 = 0;
-  t.nkb = nkb;
-  t.c0 = 0;
-  if constexpr (MODE == kGroupedWgrad) {
-    // Grid = groups x tiles of one gradient.  Within a group consecutive
-    // tiles go to one XCD, as in the dense form: its share of the group's
-    // codes (256 rows and 256 columns of a few hundred tokens a tile) meets
-    // in that XCD's L2, and every group is spread over all XCDs, so a
-    // popular expert does not fall to one of them.
-    const int per = g.tiles_m * g.tiles_n;
-    const int gi = blockIdx.x / per;
-    const int logical = xcd_logical(blockIdx.x - gi * per, per);
-    const int tn = logical / g.tiles_m;
-    const int tm = logical - tn * g.tiles_m;
-    // offsets outside [0, k], decreasing or off the 128-token tiles are
-    // clamped and rounded down: every access stays inside the operands
-    const int lo = min(max(g.offsets[gi], 0), g.k) / BK;
-    const int hi = min(max(g.offsets[gi + 1], 0), g.k) / BK;
-    t.kb0 = lo;
-    t.nkb = max(hi - lo, 0);
-    t.m0 = tm * BM;
-    t.mend = min(t.m0 + BM, g.rows);
-    t.wrows = 4;
-    t.n0 = tn * g.bn;
-    t.w = g.w;
-    t.sw = g.sw;
-    t.c0 = (int64_t)gi * g.rows * g.ldc;
-    return true;
-  } else if constexpr (MODE == kGrouped) {
+  if constexpr (MODE == kGrouped) {
     // Grid = (ceil(rows_cap/256) + groups) * tiles_n, an upper bound of the
     // real tile count; workgroups beyond it exit.  N tiles vary fastest, so
     // the XCD of a workgroup fixes its N tiles and W rows stay XCD-local.
@@ -310,7 +278,6 @@ __device__ __forceinline__ void k_loop3(int nkb, uint8_t* __restrict__ s0, uint8
 // own, so the 256-column form keeps its registers.
 template <int MODE, int OUT, int ACC, int NARROW>
 __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
-  constexpr bool kIsWgrad = MODE == kWgrad || MODE == kGroupedWgrad;  // operand scales per column and K block
   // two full stages, or (grouped tiles of at most 128 rows) three small
   // ones, then the scale buffer
   constexpr int kStageBytes = MODE == kGrouped ? 3 * kSmallStage : 2 * kFullStage;
@@ -330,8 +297,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
   const int wm = wave & (wrows - 1);
   const int wn = wave >> (wrows == 4 ? 2 : wrows == 2 ? 1 : 0);
   const int K = g.k, N = g.n;
-  const int nkb = t.nkb;       // K blocks of this tile
-  const int nkb_row = K / BK;  // K blocks of an operand row (all of them but for the grouped weight gradient)
+  const int nkb = K / BK;
 
   // ---- global->LDS assignment: one wave instruction moves 8 rows x 128 B.
   // Full tiles: wave w moves rows 32w..32w+31 of both the A and the W tile
@@ -344,11 +310,10 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
   // K-block offset goes in an SGPR, the LDS address in M0: issuing costs no
   // VALU work.  Offsets fit in 32 bits (the host rejects operands of 2 GiB+).
   const uint32_t rowb = (uint32_t)K;  // bytes per operand row
-  const uint32_t kofs0 = (uint32_t)t.kb0 * BK, sofs0 = (uint32_t)t.kb0 * 4u;  // first K block, in codes and in scales
   const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(g.a + (size_t)t.m0 * rowb + kofs0), 0, (int)((uint32_t)(t.mend - t.m0) * rowb - kofs0), kRsrcFlags);
+      (void*)(g.a + (size_t)t.m0 * rowb), 0, (int)((uint32_t)(t.mend - t.m0) * rowb), kRsrcFlags);
   const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(t.w + (size_t)t.n0 * rowb + kofs0), 0, (int)((uint32_t)(N - t.n0) * rowb - kofs0), kRsrcFlags);
+      (void*)(t.w + (size_t)t.n0 * rowb), 0, (int)((uint32_t)(N - t.n0) * rowb), kRsrcFlags);
   auto row_off = [&](int row) { return (uint32_t)row * rowb + 16u * (uint32_t)((lane & 7) ^ swz(row)); };
   uint32_t r_off[4];
 #pragma unroll
@@ -356,20 +321,20 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
   // scales: waves 0-3 bring the A scales of rows 64w..64w+63, waves 4-7 the
   // W scale of columns 64(w-4)..+63 (one value per column, so all forms
   // share the layout)
-  const uint32_t sblk = (uint32_t)nkb_row * 4u;  // bytes per scale row
+  const uint32_t sblk = (uint32_t)nkb * 4u;  // bytes per scale row
   const int sidx = (wave & 3) * 64 + lane;
   __amdgpu_buffer_rsrc_t s_rsrc;
   uint32_t s_off;
   if (wave < 4) {
-    s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(g.sa + (size_t)t.m0 * nkb_row + t.kb0), 0,
-                                               (int)((uint32_t)(t.mend - t.m0) * sblk - sofs0), kRsrcFlags);
+    s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(g.sa + (size_t)t.m0 * nkb), 0,
+                                               (int)((uint32_t)(t.mend - t.m0) * sblk), kRsrcFlags);
     s_off = (uint32_t)sidx * sblk;
-  } else if (kIsWgrad) {
-    s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(t.sw + (size_t)t.n0 * nkb_row + t.kb0), 0,
-                                               (int)((uint32_t)(N - t.n0) * sblk - sofs0), kRsrcFlags);
+  } else if (MODE == kWgrad) {
+    s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(t.sw + (size_t)t.n0 * nkb), 0,
+                                               (int)((uint32_t)(N - t.n0) * sblk), kRsrcFlags);
     s_off = (uint32_t)sidx * sblk;
   } else {  // one scale row per 128 columns, from the one holding column n0
-    s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(t.sw + (size_t)(t.n0 >> 7) * nkb_row), 0,
+    s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(t.sw + (size_t)(t.n0 >> 7) * nkb), 0,
                                                (int)((uint32_t)(((N + 127) >> 7) - (t.n0 >> 7)) * sblk), kRsrcFlags);
     s_off = 0;  // (unused: these scales arrive by quarters)
   }
@@ -389,7 +354,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
   // the scale row of its 128-column block, ((n0 mod 128) + e) / 128 rows past
   // the buffer's first)
   const int q_entry = (wave & 3) * 64 + (lane >> 2);  // entry of quarter 0
-  const bool row_entries = kIsWgrad || wave < 4;
+  const bool row_entries = MODE == kWgrad || wave < 4;
   const uint32_t q_lane = 4u * (uint32_t)(lane & 3);
   // (grouped tiles start at a multiple of 256 columns: a W wave's 64
   // columns share one scale row)
@@ -405,7 +370,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(s_rsrc, (lds_void_ptr)half, 4, off + (uint32_t)grp * 16u, 0, 0, 0);
   };
   auto issue_scales = [&](int kb, uint8_t* st, uint8_t* scl, int step) {
-    if (kIsWgrad && wave >= 4) {
+    if (MODE == kWgrad && wave >= 4) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(s_rsrc, (lds_void_ptr)(st + StageLayout<BM>::kS + (wave & 3) * 256), 4,
                                                s_off, (uint32_t)kb * 4u, 0, 0);
     } else if (step >= 0) {
@@ -481,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     constexpr bool kFragScale = MODE == kDense && JN != 8;
     float sc[4], sc2[4];
     const int jb = kFragScale ? (128 - ((t.n0 + wn * WC) & 127)) >> 4 : JN;
-    if constexpr (!kIsWgrad) {
+    if constexpr (MODE != kWgrad) {
       const float swv = SA[(BM + wn * WC) * 4];
       const float swv2 = kFragScale ? SA[(BM + wn * WC + WC - 16) * 4] : 0.f;
 #pragma unroll
@@ -492,7 +457,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     }
     // Wgrad issues the refill later (see below); the other forms once the
     // scales are read
-    if (!kIsWgrad) refill_now();
+    if (MODE != kWgrad) refill_now();
     const int wrow0 = wn * WC + r16;
     const int wsw = swz(wrow0);  // same swizzle for rows wrow0 + 16j
     // one base address per half; fragment j is 2 KiB further (an
@@ -524,7 +489,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     v8bf bf[4];      // the current W fragment widened to BF16: [q]
     read_w_lo(0, w0lo);
     read_w_hi(0, w0hi);
-    if constexpr (kIsWgrad) {
+    if constexpr (MODE == kWgrad) {
       // the Wgrad fold holds more registers: widen up front so the raw
       // bytes die before the MFMAs start (no spills)
 #pragma unroll
@@ -548,7 +513,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     const float* swp = S + wn_lane * WC + 4 * (lane >> 4);
     v4f swj = v4f{0.f, 0.f, 0.f, 0.f};
     auto fold = [&](int j, int f) {
-      if constexpr (kIsWgrad) {
+      if constexpr (MODE == kWgrad) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[f][j][v] = __builtin_fmaf(p[f][v], sa[f] * swj[v], acc[f][j][v]);
       } else {
@@ -562,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     for (int j = 0; j < JN; ++j) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (j == 0 && !kIsWgrad) {
+        if (j == 0 && MODE != kWgrad) {
           bf[q] = part(w0lo, w0hi, q);
 #pragma unroll
           for (int f = 0; f < 4; ++f) af[f][q] = part(alo[f], ahi[f], q);
@@ -580,10 +545,10 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
         // block's first fragments are in registers: a register reload after
         // the refill would wait for it (measured 693 -> 460 us for
         // 2048 x 7168 over 16384 tokens; the dense form is 5% slower so)
-        if (kIsWgrad && j == 0 && q == 0) refill_now();
+        if (MODE == kWgrad && j == 0 && q == 0) refill_now();
         // slot q is no longer needed by fragment j: widen fragment j+1's part
         if (j < JN - 1) bf[q] = part(wlo, whi, q);
-        if constexpr (kIsWgrad) {
+        if constexpr (MODE == kWgrad) {
           if (q == 0) swj = *reinterpret_cast<const v4f*>(swp + j * 16);
         }
         // a consumed half of fragment j+1's bytes is refilled with fragment
@@ -619,7 +584,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
 #pragma unroll
     for (int f = 0; f < 4; ++f) sa[f] = SA[(arow0 + f * 16) * 4];
 #pragma unroll
-    for (int j = 0; j < JN; ++j) sw[j] = kIsWgrad ? S[wrow0 + j * 16] : SA[(BM + wrow0 + j * 16) * 4];
+    for (int j = 0; j < JN; ++j) sw[j] = MODE == kWgrad ? S[wrow0 + j * 16] : SA[(BM + wrow0 + j * 16) * 4];
     refill_now();
     const int wsw = swz(wrow0);
     const uint8_t* Wb = st + L::kW + wrow0 * 128;
@@ -721,7 +686,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     const float* swp = S + wn * WC + 4 * (lane >> 4);
     v4f swj = v4f{0.f, 0.f, 0.f, 0.f};
     auto fold = [&](int j, int f) {
-      if constexpr (kIsWgrad) {
+      if constexpr (MODE == kWgrad) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[f][j][v] = __builtin_fmaf(p[f][v], sa[f] * swj[v], acc[f][j][v]);
       } else {
@@ -740,10 +705,10 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
                                                                0, 0, 0, 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (kIsWgrad) swj = *reinterpret_cast<const v4f*>(swp + j * 16);
+      if constexpr (MODE == kWgrad) swj = *reinterpret_cast<const v4f*>(swp + j * 16);
       if (j == 0) {
         refill_now();
-        if constexpr (!kIsWgrad) {
+        if constexpr (MODE != kWgrad) {
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             sc[f] = sa[f] * swv;
@@ -797,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     for (int f = 0; f < 4; ++f) ae[f] = e8m0(SA[(arow0 + f * 16) * 4]);
 #pragma unroll
     for (int j = 0; j < JN; ++j)  // this lane's W row
-      we[j] = e8m0(kIsWgrad ? SS[wrow0 + j * 16] : SA[(BM + wrow0 + j * 16) * 4]);
+      we[j] = e8m0(MODE == kWgrad ? SS[wrow0 + j * 16] : SA[(BM + wrow0 + j * 16) * 4]);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < JN; ++j) {
@@ -943,7 +908,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
               if (n + v < N) crow[n + v] = (uint16_t)bf16_rne_bits(r[v]);
           }
         } else {
-          float* crow = reinterpret_cast<float*>(g.c) + t.c0 + (int64_t)m * g.ldc;
+          float* crow = reinterpret_cast<float*>(g.c) + (int64_t)m * g.ldc;
           if (n + 3 < N && g.vec_c) {
             *reinterpret_cast<v4f*>(crow + n) = r;
           } else {
@@ -968,7 +933,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bs_kernel(GemmArgs g) {
     // 224-column tiles: the waves split them as 2 x 112 columns (7 W
     // fragments each); the stage still receives 256 W rows (the last 32
     // belong to the next tile and are not used)
-    static_assert(kIsWgrad || (MODE == kDense && (OUT == kOutF32 || OUT == kOutBF16)),
+    static_assert(MODE == kWgrad || (MODE == kDense && (OUT == kOutF32 || OUT == kOutBF16)),
                   "224-column tiles: dense (float32 / BF16 out) and weight-gradient forms");
     run(std::integral_constant<int, 7>{});
   } else {
@@ -1006,7 +971,7 @@ void launch_acc_w(const GemmArgs& g, int grid, int acc, hipStream_t stream) {
 
 template <int MODE, int OUT>
 hipError_t launch_acc(const GemmArgs& g, int grid, int acc, hipStream_t stream) {
-  if constexpr (MODE == kWgrad || MODE == kGroupedWgrad || (MODE == kDense && (OUT == kOutF32 || OUT == kOutBF16))) {
+  if constexpr (MODE == kWgrad || (MODE == kDense && (OUT == kOutF32 || OUT == kOutBF16))) {
     if (g.bn == 224) {
       launch_acc_w<MODE, OUT, 1>(g, grid, acc, stream);
       return hipGetLastError();
@@ -1105,18 +1070,6 @@ hipError_t launch_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint8
   g.bn = tile_width(g.tiles_m, kin);
   g.tiles_n = (kin + g.bn - 1) / g.bn;
   return launch_acc<kWgrad, kOutF32>(g, g.tiles_m * g.tiles_n, acc, stream);
-}
-
-hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint8_t* x_t,
-                                const float* x_scales, const int32_t* offsets, int groups, int cap, int nout,
-                                int kin, int acc, float* dw, int64_t lddw, hipStream_t stream) {
-  GemmArgs g{};
-  g.a = dy_t; g.sa = dy_scales; g.w = x_t; g.sw = x_scales; g.offsets = offsets;
-  g.c = dw; g.ldc = lddw; g.vec_c = (lddw % 4) == 0; g.rows = nout; g.n = kin; g.k = cap; g.groups = groups;
-  g.tiles_m = (nout + BM - 1) / BM;
-  g.bn = tile_width(g.tiles_m * groups, kin);
-  g.tiles_n = (kin + g.bn - 1) / g.bn;
-  return launch_acc<kGroupedWgrad, kOutF32>(g, g.tiles_m * g.tiles_n * groups, acc, stream);
 }
 
 }  // namespace fp8q
