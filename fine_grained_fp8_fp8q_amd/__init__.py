@@ -470,6 +470,10 @@ def swiglu_quantize(x, scale_mode="free", cache=False, cache_scale_mode="pow2"):
 
 # ------------------------------------- the expert layer around the GEMMs ----
 
+# These calls are also made for a single token, where the host's part of a
+# call is most of its time: each argument is looked at once, and the stream is
+# asked for by its raw handle.
+
 def _one_device(first, *others):
     """The device of the tensors given (None among them is skipped)."""
     dev = first.device
@@ -479,16 +483,22 @@ def _one_device(first, *others):
     return dev
 
 
+def _raw_stream(dev):
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev.index) if get else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _call(dev, name, *args):
     """Calls the entry point on the current stream of dev, which becomes the
     current device for the call where it is not."""
     torch = _torch()
-    fn = getattr(load_library(), name)
+    fn = getattr(_lib or load_library(), name)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(dev))
     if st != OK:
         raise Fp8qError(st, name)
 
@@ -498,45 +508,48 @@ def _addr(t):
     return t.data_ptr() if t is not None and t.numel() else None
 
 
-def _ld(t, width):
-    """Row stride of a 2-D tensor that may be absent or empty; the stride of
-    a single row says nothing, and a stride below the width (an expanded or
-    overlapping tensor) is left for the library to refuse."""
-    return t.stride(0) if t is not None and t.numel() and t.shape[0] > 1 else max(width, 1)
-
-
-def _float_rows(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+def _rows_of(t, name, dtypes):
+    """(rows, columns, row stride, address) of a 2-D GPU tensor with
+    contiguous rows and one of the types given.  The stride of a single row
+    says nothing; one below the width (an expanded or overlapping tensor) is
+    left for the library to refuse."""
+    if not isinstance(t, _types()[0]):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    code = _out_code(t.dtype)
-    _row_major(t, name)
-    return code
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1 and shape[0]):
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    rows, cols = shape
+    if rows and cols:
+        return rows, cols, stride[0] if rows > 1 else cols, t.data_ptr()
+    return rows, cols, max(cols, 1), None
+
+
+_torch_types = None
+
+
+def _types():
+    """(torch.Tensor, (float32, bfloat16) in the order of OUT_F32 and OUT_BF16, int32)."""
+    global _torch_types
+    if _torch_types is None:
+        torch = _torch()
+        _torch_types = torch.Tensor, (torch.float32, torch.bfloat16), torch.int32
+    return _torch_types
 
 
 def _pair_table(row_of, weights):
-    torch = _torch()
-    _need(row_of, torch.int32, "row_of")
-    if row_of.dim() != 2 or not row_of.is_contiguous():
+    """Checks row_of and weights: contiguous [tokens, topk]."""
+    if row_of.dtype != _types()[2] or not row_of.is_cuda or row_of.dim() != 2 or not row_of.is_contiguous():
+        _need(row_of, _types()[2], "row_of")
         raise ValueError("row_of must be a contiguous int32 [tokens, topk] tensor")
-    if weights is not None:
+    if weights is not None and (weights.dtype != _types()[1][0] or weights.shape != row_of.shape or
+                                not weights.is_contiguous()):
         _contig_f32(weights, "weights")
-        if weights.shape != row_of.shape:
-            raise ValueError("weights must have the shape of row_of")
-
-
-def _own_rows(out, shape, dtype, device, name):
-    """A new [rows, cols] tensor, or the caller's if it has that form."""
-    torch = _torch()
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(out, dtype, name)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(out.shape)}")
-    _row_major(out, name)
-    return out
+        raise ValueError("weights must have the shape of row_of")
+    return row_of.shape
 
 
 def moe_sort(experts, num_hosted, first=0, align=1, rows_cap=None):
@@ -552,31 +565,28 @@ def moe_sort(experts, num_hosted, first=0, align=1, rows_cap=None):
     are dropped.
     """
     torch = _torch()
-    if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
-        raise TypeError("experts must be an int32 or int64 tensor")
-    if not experts.is_cuda:
-        raise ValueError("experts must be on the GPU")
-    _row_major(experts, "experts")
-    tokens, topk = experts.shape
+    tokens, topk, ld, experts_p = _rows_of(experts, "experts", (torch.int32, torch.int64))
     if num_hosted < 0 or align < 1:
         raise ValueError("num_hosted must not be negative, align must be at least 1")
+    pairs = tokens * topk
     if rows_cap is None:
-        rows_cap = (tokens * topk + num_hosted * (align - 1) + align - 1) // align * align
-    dev = experts.device
-    # one allocation: [offsets | token | row_of], each part 16-byte aligned
+        rows_cap = (pairs + num_hosted * (align - 1) + align - 1) // align * align
+    elif rows_cap < 0:
+        raise ValueError("rows_cap must not be negative")
+    # one allocation: [offsets | token | row_of | workspace], each part 16-byte aligned
     n0, n1 = (num_hosted + 4) // 4 * 4, (rows_cap + 3) // 4 * 4
-    need = load_library().fp8q_moe_sort_workspace(tokens, topk, num_hosted)
-    n2 = (tokens * topk + 3) // 4 * 4 if need else tokens * topk
-    buf = torch.empty(n0 + n1 + n2 + need // 4, dtype=torch.int32, device=dev)
+    need = (_lib or load_library()).fp8q_moe_sort_workspace(tokens, topk, num_hosted)
+    n2 = (pairs + 3) // 4 * 4
+    buf = torch.empty(n0 + n1 + n2 + need // 4, dtype=torch.int32, device=experts.device)
     if num_hosted == 0:  # nothing is launched: every pair is without a row
         buf.fill_(-1)
         buf[0] = 0
     p = buf.data_ptr()
-    _call(dev, "fp8q_moe_sort", _addr(experts), INDEX_I64 if experts.dtype == torch.int64 else INDEX_I32, tokens, topk,
-          _ld(experts, topk), first, num_hosted, align, rows_cap, p, p + 4 * n0, p + 4 * (n0 + n1),
+    _call(experts.device, "fp8q_moe_sort", experts_p, INDEX_I64 if experts.dtype == torch.int64 else INDEX_I32, tokens,
+          topk, ld, first, num_hosted, align, rows_cap, p, p + 4 * n0, p + 4 * (n0 + n1),
           p + 4 * (n0 + n1 + n2) if need else None, need)
     return (buf[:num_hosted + 1], buf[n0:n0 + rows_cap],
-            buf[n0 + n1:n0 + n1 + tokens * topk].view(tokens, topk))
+            buf.as_strided((tokens, topk), (topk, 1), buf.storage_offset() + n0 + n1))
 
 
 def moe_combine(y, row_of, weights=None, out_dtype=None, out=None):
@@ -587,19 +597,23 @@ def moe_combine(y, row_of, weights=None, out_dtype=None, out=None):
     (the gradient of the row gather).  out_dtype torch.bfloat16 (default) or
     torch.float32.
     """
-    torch = _torch()
-    yd = _float_rows(y, "y")
-    _pair_table(row_of, weights)
-    cap, n = y.shape
-    tokens, topk = row_of.shape
-    if out is not None and out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError("out has another type than out_dtype")
-    dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
-    od = _out_code(dtype)
-    out = _own_rows(out, (tokens, n), dtype, y.device, "out")
+    types = _types()[1]
+    cap, n, ld, y_p = _rows_of(y, "y", types)
+    tokens, topk = _pair_table(row_of, weights)
     dev = _one_device(y, row_of, weights, out)
-    _call(dev, "fp8q_moe_combine", _addr(y), yd, cap, n, _ld(y, n), _addr(row_of), _addr(weights), tokens, topk, od,
-          _addr(out), _ld(out, n))
+    if out is None:
+        out_dtype = out_dtype or types[OUT_BF16]
+        if out_dtype not in types:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        out, ldo = y.new_empty((tokens, n), dtype=out_dtype), max(n, 1)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("out has another type than out_dtype")
+        ot, on, ldo, _ = _rows_of(out, "out", types)
+        if (ot, on) != (tokens, n):
+            raise ValueError(f"out must be [{tokens}, {n}], got [{ot}, {on}]")
+    _call(dev, "fp8q_moe_combine", y_p, types.index(y.dtype), cap, n, ld, _addr(row_of), _addr(weights), tokens, topk,
+          types.index(out.dtype), _addr(out), ldo)
     return out
 
 
@@ -613,28 +627,29 @@ def moe_combine_backward(dout, y, row_of, weights=None, token=None, bf16=True, q
     without a pair are zero; without it they are left uninitialised.
     """
     torch = _torch()
-    dd = _float_rows(dout, "dout")
-    yd = _float_rows(y, "y")
-    _pair_table(row_of, weights)
-    tokens, topk = row_of.shape
-    cap, n = y.shape
-    if tuple(dout.shape) != (tokens, n):
-        raise ValueError(f"dout must be [{tokens}, {n}], got {tuple(dout.shape)}")
+    types = _types()[1]
+    dt, dn, ldd, dout_p = _rows_of(dout, "dout", types)
+    cap, n, ldy, y_p = _rows_of(y, "y", types)
+    tokens, topk = _pair_table(row_of, weights)
+    if (dt, dn) != (tokens, n):
+        raise ValueError(f"dout must be [{tokens}, {n}], got [{dt}, {dn}]")
     if token is not None:
         _need(token, torch.int32, "token")
         if token.dim() != 1 or token.numel() != cap or not token.is_contiguous():
             raise ValueError(f"token must be a contiguous int32 tensor of {cap} rows")
     dev = _one_device(y, dout, row_of, weights, token)
-    dy = torch.empty((cap, n), dtype=torch.bfloat16, device=dev) if bf16 else None
+    dy = y.new_empty((cap, n), dtype=torch.bfloat16) if bf16 else None
     codes = scales = dw = None
+    ldc = n
     if quantize:
         codes = _alloc_codes(cap, n, dev)
-        scales = torch.empty((cap, (n + 127) // 128), dtype=torch.float32, device=dev)
+        ldc = codes.stride(0)
+        scales = y.new_empty((cap, (n + 127) // 128), dtype=torch.float32)
     if want_dweights:
-        dw = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
-    _call(dev, "fp8q_moe_combine_backward", _addr(dout), dd, tokens, n, _ld(dout, n), _addr(y), yd, cap,
-          _ld(y, n), _addr(row_of), _addr(weights), topk, _addr(token), _addr(dy), _ld(dy, n),
-          _scale_mode(scale_mode), _addr(codes), _ld(codes, n), _addr(scales), _addr(dw))
+        dw = y.new_empty((tokens, topk), dtype=torch.float32)
+    _call(dev, "fp8q_moe_combine_backward", dout_p, types.index(dout.dtype), tokens, n, ldd, y_p, types.index(y.dtype), cap,
+          ldy, _addr(row_of), _addr(weights), topk, _addr(token), _addr(dy), max(n, 1), _scale_mode(scale_mode), _addr(codes), ldc,
+          _addr(scales), _addr(dw))
     return dy, codes, scales, dw
 
 
@@ -648,36 +663,29 @@ def swiglu_backward(x, dy, x_scales=None, bf16=True, quantize=False, scale_mode=
     and the 1x128 quantization of dx (quantize=True; inter a multiple of 128).
     """
     torch = _torch()
-    if x_scales is None:
-        _need(x, torch.bfloat16, "x")
-    else:
-        _need(x, torch.uint8, "x")
-        _contig_f32(x_scales, "x_scales")
-    _need(dy, torch.bfloat16, "dy")
-    _row_major(x, "x")
-    _row_major(dy, "dy")
-    rows, two_inter = x.shape
-    if two_inter % 2:
-        raise ValueError("x must have an even number of columns (gate | up)")
-    inter = two_inter // 2
-    if tuple(dy.shape) != (rows, inter):
-        raise ValueError(f"dy must be [{rows}, {inter}], got {tuple(dy.shape)}")
-    if x_scales is not None and tuple(x_scales.shape) != (rows, two_inter // 128):
-        raise ValueError(f"x_scales must be [{rows}, {two_inter // 128}], got {tuple(x_scales.shape)}")
+    rows, two_inter, ldx, x_p = _rows_of(x, "x", (torch.bfloat16,) if x_scales is None else (torch.uint8,))
+    dr, inter, lddy, dy_p = _rows_of(dy, "dy", (torch.bfloat16,))
+    if two_inter != 2 * inter or dr != rows:
+        raise ValueError(f"x must be [rows, 2*inter] and dy [rows, inter], got [{rows}, {two_inter}] and [{dr}, {inter}]")
     if inter % 128 and (x_scales is not None or quantize):
         raise ValueError("inter must be a multiple of 128 for the FP8 cache and for a quantized dx")
+    if x_scales is not None:
+        _contig_f32(x_scales, "x_scales")
+        if tuple(x_scales.shape) != (rows, two_inter // 128):
+            raise ValueError(f"x_scales must be [{rows}, {two_inter // 128}], got {tuple(x_scales.shape)}")
     if not (bf16 or quantize or want_y):
         raise ValueError("nothing to compute: ask for bf16, quantize or want_y")
     dev = _one_device(x, dy, x_scales)
-    dx = torch.empty((rows, two_inter), dtype=torch.bfloat16, device=dev) if bf16 else None
-    y = torch.empty((rows, inter), dtype=torch.bfloat16, device=dev) if want_y else None
+    dx = dy.new_empty((rows, two_inter)) if bf16 else None
+    y = dy.new_empty((rows, inter)) if want_y else None
     codes = scales = None
+    ldc = two_inter
     if quantize:
         codes = _alloc_codes(rows, two_inter, dev)
-        scales = torch.empty((rows, two_inter // 128), dtype=torch.float32, device=dev)
-    _call(dev, "fp8q_swiglu_backward", _addr(x), _addr(x_scales), rows, inter, _ld(x, two_inter), _addr(dy),
-          _ld(dy, inter), _addr(dx), _ld(dx, two_inter), _scale_mode(scale_mode), _addr(codes), _ld(codes, two_inter),
-          _addr(scales), _addr(y), _ld(y, inter))
+        ldc = codes.stride(0)
+        scales = dy.new_empty((rows, two_inter // 128), dtype=torch.float32)
+    _call(dev, "fp8q_swiglu_backward", x_p, _addr(x_scales), rows, inter, ldx, dy_p, lddy, _addr(dx), max(two_inter, 1),
+          _scale_mode(scale_mode), _addr(codes), ldc, _addr(scales), _addr(y), max(inter, 1))
     return dx, y, codes, scales
 
 

@@ -78,15 +78,23 @@ hipError_t launch_swiglu_quant(const uint16_t* x, int rows, int inter, int64_t l
                                int64_t ldc, float* scales, bool cache_pow2, uint8_t* ccodes, int64_t ldcc,
                                float* cscales, hipStream_t stream);
 
-// Routing table (moe_route.hip): one workgroup alone up to
-// kSortPairsPerBlock pairs; above, at most kMaxSortBlocks of them, after a
-// launch that counts each one's share (hist: int32 [blocks, groups]).
+// Routing table (moe_route.hip): one workgroup alone up to kSortAlonePairs
+// pairs; above, workgroups of 1024, 2048 or 4096 pairs -- the fewest whose
+// count table (hist: int32 [blocks, groups], from a launch of its own, read
+// whole by each of them) stays below kSortTable entries -- and at most
+// kMaxSortBlocks of them.
 constexpr int kMaxSortGroups = 512;
-constexpr int kSortPairsPerBlock = 4096;
+constexpr int kSortAlonePairs = 4096;
+constexpr int kSortTable = 8192;
 constexpr int kMaxSortBlocks = 256;
-inline int sort_blocks(int pairs) {
-  const int want = (int)(((int64_t)pairs + kSortPairsPerBlock - 1) / kSortPairsPerBlock);
-  return want < 1 ? 1 : want < kMaxSortBlocks ? want : kMaxSortBlocks;
+inline int sort_blocks(int pairs, int groups) {
+  if (pairs <= kSortAlonePairs) return 1;
+  int64_t blocks = 0;
+  for (int chunk = 1024; chunk <= 4096; chunk *= 2) {
+    blocks = ((int64_t)pairs + chunk - 1) / chunk;
+    if (blocks <= kMaxSortBlocks && blocks * groups <= kSortTable) break;
+  }
+  return (int)(blocks < kMaxSortBlocks ? blocks : kMaxSortBlocks);
 }
 hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, int64_t ld, int64_t first, int groups,
                            int align, int cap, int* offsets, int* token, int* row_of, int* hist, hipStream_t stream);

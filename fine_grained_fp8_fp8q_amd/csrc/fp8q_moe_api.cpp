@@ -18,7 +18,7 @@ extern "C" {
 int64_t fp8q_moe_sort_workspace(int64_t tokens, int64_t topk, int32_t G) {
   if (!dim_ok(tokens) || !dim_ok(topk) || G <= 0 || tokens == 0 || topk == 0) return 0;
   if (topk > kMaxDim / tokens) return 0;
-  const int blocks = fp8q::sort_blocks((int)(tokens * topk));
+  const int blocks = fp8q::sort_blocks((int)(tokens * topk), G);
   return blocks > 1 ? (int64_t)blocks * G * (int64_t)sizeof(int32_t) : 0;
 }
 
@@ -83,8 +83,8 @@ fp8q_status fp8q_moe_combine_backward(const void* dout, int dout_dtype, int64_t 
   if ((pairs > 0 && ld_dout < N) || (dweights && rows_cap > 0 && ld_y < N) || (rows_out && dy_bf16 && ld_dy < N) ||
       (rows_out && dy_codes && ld_codes < N))
     return FP8Q_ERR_SHAPE;
-  // one workgroup per pair, and one per 64 rows to look for rows without one
-  if (pairs + rows_cap / 64 + 1 >= kMaxGroups) return FP8Q_ERR_SHAPE;
+  // one workgroup per pair, and one per 16 rows to look for rows without one
+  if (pairs + rows_cap / 16 + 1 >= kMaxGroups) return FP8Q_ERR_SHAPE;
   if (!aligned16(dout) || !aligned16(y) || !aligned16(row_of) || !aligned16(weights) || !aligned16(token) ||
       !aligned16(dy_bf16) || !aligned16(dy_codes) || !aligned16(dy_scales) || !aligned16(dweights))
     return FP8Q_ERR_ALIGN;

@@ -10,6 +10,7 @@
 //   quantized per 1x128 tile (jp-study.kr doc 258368 ¶1, tmdrlife.com
 //   wr_id=13334 ¶4: the activation gradient before the down-projections is
 //   one of the tensors that take FP8), and dw[t,j] = <dout[t], y[row]>.
+#include "chunk8.h"
 #include "fp8q_internal.h"
 #include "quant_common.h"
 
@@ -27,7 +28,7 @@ struct SortArgs {
   int groups, align;
   int pairs;            // tokens * topk
   int cap;              // rows of the sorted layout
-  int chunk;            // pairs per workgroup, a multiple of kSortThreads
+  int chunk;            // pairs per workgroup, a multiple of kSortThreads (of 64 per wave)
   int* offsets;         // [groups + 1]
   int* token;           // [cap]
   int* row_of;          // [pairs]
@@ -79,6 +80,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 // takes the w-th sixteenth of it in order, so a pair's row is the group's
 // start + the pairs of that expert in earlier chunks, in earlier waves, in
 // earlier steps of this wave (a running count in LDS) and in lower lanes.
+// The experts of the first four steps stay in registers between the two
+// passes (all of them below a million pairs).
 template <typename IDX>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   extern __shared__ int lds[];
@@ -89,18 +92,28 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   int* scan = start + G + 1;           // [kSortWaves]
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int blk = blockIdx.x, blocks = gridDim.x;
+  const int bits = index_bits(G);
+  const int steps = a.chunk / kSortThreads;
+  const int64_t p0 = (int64_t)blk * a.chunk + (int64_t)wave * 64 * steps + lane;
+  auto expert_at = [&](int s) {
+    const int64_t p = p0 + 64 * s;
+    return p < a.pairs ? local_expert<IDX>(a, (int)p) : -1;
+  };
+  constexpr int kHeld = 4;
+  int held[kHeld];
+#pragma unroll
+  for (int s = 0; s < kHeld; ++s) held[s] = s < steps ? expert_at(s) : -1;
   for (int i = tid; i < (kSortWaves + 2) * G + 1; i += kSortThreads) lds[i] = 0;
   __syncthreads();
 
-  const int bits = index_bits(G);
-  const int per_wave = a.chunk / kSortWaves;
-  const int64_t p0 = (int64_t)blk * a.chunk + (int64_t)wave * per_wave;
-  for (int i = 0; i < per_wave; i += 64) {
-    const int64_t p = p0 + i + lane;
-    const int e = p < a.pairs ? local_expert<IDX>(a, (int)p) : -1;
+  auto count = [&](int e) {
     const uint64_t same = same_expert(e, bits);
     if (same && lane == __builtin_ctzll(same)) atomicAdd(&cnt[wave * G + e], __builtin_popcountll(same));
-  }
+  };
+#pragma unroll
+  for (int s = 0; s < kHeld; ++s)
+    if (s < steps) count(held[s]);
+  for (int s = kHeld; s < steps; ++s) count(expert_at(s));
   // pairs of each expert in all chunks, and in the chunks before this one
   // (kept in start[] until the group starts are known)
   if (blocks > 1) {
@@ -118,6 +131,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   int mine = 0, padded = 0;
   if (tid < G) {
     int run = start[tid];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
       const int c = cnt[w * G + tid];
       cnt[w * G + tid] = run;
@@ -144,14 +158,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   if (blk == 0)
     for (int g = tid; g <= G; g += kSortThreads) a.offsets[g] = min(start[g], a.cap);
 
-  for (int i = 0; i < per_wave; i += 64) {
-    const int64_t p = p0 + i + lane;
-    const int e = p < a.pairs ? local_expert<IDX>(a, (int)p) : -1;
+  auto place = [&](int s, int e) {
     const uint64_t same = same_expert(e, bits);
     const int first = same ? __builtin_ctzll(same) : 0;
     int before = 0;
     if (same && lane == first) before = atomicAdd(&cnt[wave * G + e], __builtin_popcountll(same));
     before = __shfl(before, first);
+    const int64_t p = p0 + 64 * s;
     if (p < a.pairs) {
       int row = -1;
       if (e >= 0) {
@@ -164,7 +177,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
       }
       a.row_of[p] = row;
     }
-  }
+  };
+#pragma unroll
+  for (int s = 0; s < kHeld; ++s)
+    if (s < steps) place(s, held[s]);
+  for (int s = kHeld; s < steps; ++s) place(s, expert_at(s));
   // rows without a pair: the padding of every group, and everything behind
   // the last one
   if (a.align > 1) {
@@ -175,70 +192,6 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   }
   for (int64_t r = (int64_t)start[G] + blk * kSortThreads + tid; r < a.cap; r += (int64_t)blocks * kSortThreads)
     a.token[r] = -1;
-}
-
-// ------------------------------------------------------- 8-element chunks ---
-struct F8 {
-  float v[8];
-};
-
-template <bool F32>
-__device__ __forceinline__ F8 load8(const void* base, int64_t at, int nvalid, bool vec) {
-  F8 r;
-  if constexpr (F32) {
-    const float* p = static_cast<const float*>(base) + at;
-    if (vec) {
-      const uint4 a = ld_stream16(p), b = ld_stream16(p + 4);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r.v[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r.v[i] = i < nvalid ? p[i] : 0.0f;
-    }
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    const uint4 a = vec ? ld_stream16(p) : load8_masked(p, nvalid);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.v[2 * i] = bf16_lo(w[i]);
-      r.v[2 * i + 1] = bf16_hi(w[i]);
-    }
-  }
-  return r;
-}
-
-// Eight float32 values -> BF16 in chunk layout, nearest even by the hardware
-// convert (infinities and NaN stay what they are).
-typedef __bf16 mr_v2bf __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint4 pack8_bf16(const F8& f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(uint32_t, mr_v2bf{(__bf16)f.v[2 * i], (__bf16)f.v[2 * i + 1]});
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ void store8_bf16(uint16_t* p, uint4 c, int nvalid, bool vec) {
-  if (vec) {
-    st_stream16(p, c);
-    return;
-  }
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < nvalid) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-}
-
-__device__ __forceinline__ void store8_f32(float* p, const F8& f, int nvalid, bool vec) {
-  if (vec) {
-    st_stream16(p, make_uint4(__float_as_uint(f.v[0]), __float_as_uint(f.v[1]), __float_as_uint(f.v[2]), __float_as_uint(f.v[3])));
-    st_stream16(p + 4, make_uint4(__float_as_uint(f.v[4]), __float_as_uint(f.v[5]), __float_as_uint(f.v[6]), __float_as_uint(f.v[7])));
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < nvalid) p[i] = f.v[i];
 }
 
 // --------------------------------------------------------------- combine ---
@@ -264,7 +217,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
     for (int u = 0; u < 8; ++u) {
       const int r = j0 + u < topk ? rows[j0 + u] : -1;
       has[u] = (unsigned)r < (unsigned)cap;
-      if (has[u]) v[u] = load8<YF32>(y, (int64_t)r * ldy + col, n - col, vec);
+      if (has[u]) v[u] = ld_float8<YF32>(y, (int64_t)r * ldy + col, n - col, vec);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -275,9 +228,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
     }
   }
   if constexpr (OF32) {
-    store8_f32(static_cast<float*>(out) + (int64_t)t * ldo + col, acc, n - col, vec);
+    st_float8(static_cast<float*>(out) + (int64_t)t * ldo + col, acc, n - col, vec);
   } else {
-    store8_bf16(static_cast<uint16_t*>(out) + (int64_t)t * ldo + col, pack8_bf16(acc), n - col, vec);
+    st_bf16x8(static_cast<uint16_t*>(out) + (int64_t)t * ldo + col, pack_bf16x8(acc), n - col, vec);
   }
 }
 
@@ -300,7 +253,7 @@ struct CombineBwdArgs {
   bool vec;
 };
 
-constexpr int kZeroRows = 64;  // rows looked over by one of the trailing workgroups
+constexpr int kZeroRows = 16;  // rows looked over by one of the trailing workgroups
 
 // Workgroup p < pairs: pair p.  The pairs of a token follow one another on
 // one XCD, so its gradient row comes from HBM once and from that XCD's L2
@@ -311,23 +264,18 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   __shared__ float part[4];
   const int tid = threadIdx.x;
   const int nb = (a.n + 127) >> 7;
+  const int step = (int)blockDim.x * 8;
   if ((int)blockIdx.x >= a.pairs) {
-    const int r0 = ((int)blockIdx.x - a.pairs) * kZeroRows;
-    for (int r = r0; r < min(r0 + kZeroRows, a.cap); ++r) {
-      if (a.token[r] >= 0) continue;
-      for (int col = tid * 8; col < a.n; col += 2048) {
-        if (a.dy) store8_bf16(a.dy + (int64_t)r * a.lddy + col, make_uint4(0, 0, 0, 0), a.n - col, a.vec);
-        if (a.codes) {
-          uint8_t* dst = a.codes + (int64_t)r * a.ldc + col;
-          if (a.vec) {
-            st_stream8(dst, make_uint2(0, 0));
-          } else {
-            store8_masked(dst, make_uint2(0, 0), a.n - col);
-          }
-        }
+    const int r0 = ((int)blockIdx.x - a.pairs) * kZeroRows, at = r0 + (tid & 63);
+    uint64_t clear = __builtin_amdgcn_ballot_w64((tid & 63) < kZeroRows && at < a.cap && a.token[at < a.cap ? at : 0] < 0);
+    for (; clear; clear &= clear - 1) {
+      const int r = r0 + __builtin_ctzll(clear);
+      for (int col = tid * 8; col < a.n; col += step) {
+        if (a.dy) st_bf16x8(a.dy + (int64_t)r * a.lddy + col, make_uint4(0, 0, 0, 0), a.n - col, a.vec);
+        if (a.codes) st_codes8(a.codes + (int64_t)r * a.ldc + col, make_uint2(0, 0), a.n - col, a.vec);
       }
       if (a.codes)
-        for (int j = tid; j < nb; j += 256) a.scales[(int64_t)r * nb + j] = 0.0f;
+        for (int j = tid; j < nb; j += (int)blockDim.x) a.scales[(int64_t)r * nb + j] = 0.0f;
     }
     return;
   }
@@ -343,33 +291,26 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   const int t = (int)((unsigned)p / (unsigned)a.topk);
   const float w = a.weights ? a.weights[p] : 1.0f;
   float dot = 0.0f;
-  for (int c0 = 0; c0 < a.n; c0 += 2048) {
+  for (int c0 = 0; c0 < a.n; c0 += step) {
     const int col = c0 + tid * 8, left = a.n - col;
-    F8 g, v;
     const bool in = left > 0;
+    F8 g = {}, v = {};
     if (in) {
-      g = load8<DF32>(a.dout, (int64_t)t * a.lddo + col, left, a.vec);
-      if (a.y) v = load8<YF32>(a.y, (int64_t)row * a.ldy + col, left, a.vec);
-    }
-    if (in && a.y) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(g.v[i], v.v[i], dot);
+      g = ld_float8<DF32>(a.dout, (int64_t)t * a.lddo + col, left, a.vec);
+      if (a.y) v = ld_float8<YF32>(a.y, (int64_t)row * a.ldy + col, left, a.vec);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g.v[i] = in ? w * g.v[i] : 0.0f;
-    const uint4 d = pack8_bf16(g);
-    if (a.dy && in) store8_bf16(a.dy + (int64_t)row * a.lddy + col, d, left, a.vec);
+    for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(g.v[i], v.v[i], dot);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g.v[i] = w * g.v[i];
+    const uint4 d = pack_bf16x8(g);
+    if (a.dy && in) st_bf16x8(a.dy + (int64_t)row * a.lddy + col, d, left, a.vec);
     if (a.codes) {
       // a 16-lane DPP row holds one 1x128 tile; every lane takes part
       const TileScale ts = tile_scale<POW2>(dpp_max16(absmax8(d)));
       const uint2 c = encode8<POW2>(d, ts);
       if (in) {
-        uint8_t* dst = a.codes + (int64_t)row * a.ldc + col;
-        if (a.vec) {
-          st_stream8(dst, c);
-        } else {
-          store8_masked(dst, c, left);
-        }
+        st_codes8(a.codes + (int64_t)row * a.ldc + col, c, left, a.vec);
         if ((tid & 15) == 0) a.scales[(int64_t)row * nb + (col >> 7)] = ts.s;
       }
     }
@@ -378,7 +319,10 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
   if ((tid & 63) == 0) part[tid >> 6] = dot;
   __syncthreads();
-  if (tid == 0) a.dweights[p] = (part[0] + part[1]) + (part[2] + part[3]);
+  if (tid == 0) {
+    for (int i = 1; i < (int)blockDim.x >> 6; ++i) dot += part[i];
+    a.dweights[p] = dot;
+  }
 }
 
 }  // namespace
@@ -397,22 +341,28 @@ hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, i
   SortArgs a{};
   a.experts = experts; a.topk = topk; a.ld = ld; a.first = first; a.groups = groups; a.align = align;
   a.pairs = pairs; a.cap = cap; a.offsets = offsets; a.token = token; a.row_of = row_of; a.hist = hist;
-  const int blocks = sort_blocks(pairs);
+  const int blocks = sort_blocks(pairs, groups);
   const int64_t per = ((int64_t)pairs + blocks - 1) / blocks;
   a.chunk = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
   if (a.chunk == 0) a.chunk = kSortThreads;
   return i64 ? launch_sort<int64_t>(a, blocks, stream) : launch_sort<int32_t>(a, blocks, stream);
 }
 
-hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t ldy, const int* row_of,
-                              const float* weights, int tokens, int topk, bool out_f32, void* out, int64_t ldo,
-                              hipStream_t stream) {
-  const bool vec = n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0;
-  // workgroups of 256, 128 or 64 threads, whichever leaves the fewest idle
+// Threads of a workgroup that goes over a row of n columns, eight a thread:
+// 256, 128 or 64, whichever leaves the fewest idle (7168 columns: 7 x 128).
+static int row_threads(int n) {
   const int items = (n + 7) / 8;
   int threads = 256;
   for (int c = 128; c >= 64; c >>= 1)
     if ((items + c - 1) / c * c < (items + threads - 1) / threads * threads) threads = c;
+  return threads;
+}
+
+hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t ldy, const int* row_of,
+                              const float* weights, int tokens, int topk, bool out_f32, void* out, int64_t ldo,
+                              hipStream_t stream) {
+  const bool vec = n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0;
+  const int items = (n + 7) / 8, threads = row_threads(n);
   const int chunks = (items + threads - 1) / threads;
   const dim3 grid((unsigned)(tokens * chunks)), block(threads);
   if (y_f32) {
@@ -431,10 +381,11 @@ hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t
 
 template <bool DF32, bool YF32>
 static void launch_bwd(const CombineBwdArgs& a, int grid, bool pow2, hipStream_t stream) {
+  const dim3 block(row_threads(a.n));
   if (pow2)
-    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, true>), dim3(grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, true>), dim3(grid), block, 0, stream, a);
   else
-    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, false>), dim3(grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, false>), dim3(grid), block, 0, stream, a);
 }
 
 hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int tokens, int n, int64_t lddo,

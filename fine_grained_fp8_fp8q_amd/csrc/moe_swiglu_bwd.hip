@@ -11,6 +11,7 @@
 // power-of-two scales).  One pass reads x and dy once and writes, as asked,
 // dx in BF16, dx quantized per 1x128 tile (of the BF16 value, as the plain
 // quantizer would), and y in BF16.
+#include "chunk8.h"
 #include "fp8q_internal.h"
 #include "quant_common.h"
 #include "swiglu_common.h"
@@ -37,25 +38,6 @@ struct SwigluBwdArgs {
   int inter, nb, ntiles;
   bool vec;
 };
-
-__device__ __forceinline__ void store8(uint16_t* p, uint4 c, int nvalid, bool full) {
-  if (full) {
-    st_stream16(p, c);
-    return;
-  }
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < nvalid) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-}
-
-__device__ __forceinline__ uint2 load8_codes_masked(const uint8_t* p, int nvalid) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < nvalid) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
-}
 
 // Eight elements of x: BF16 (16 bytes) or E4M3 codes (8 bytes, in .x and .y)
 // with their tile's scale.
@@ -96,44 +78,32 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
   struct Chunk {
     uint4 g, u, d;
     float sg, su;
-    int row, col, nvalid;
-    bool valid, full;
+    int row, col, left;  // left: columns of inter from col on (0: no tile)
   };
   auto fetch = [&](uint32_t base, Chunk& c) {
     const uint32_t t = base + (uint32_t)grp;
-    c.valid = t < (uint32_t)a.ntiles;
-    c.row = c.valid ? (int)(t / (uint32_t)a.nb) : 0;
-    const int cb = c.valid ? (int)(t - (uint32_t)c.row * (uint32_t)a.nb) : 0;
+    const bool valid = t < (uint32_t)a.ntiles;
+    c.row = valid ? (int)(t / (uint32_t)a.nb) : 0;
+    const int cb = valid ? (int)(t - (uint32_t)c.row * (uint32_t)a.nb) : 0;
     c.col = cb * 128 + sub * 8;
-    c.nvalid = c.valid ? a.inter - c.col : 0;
-    c.full = a.vec && c.valid && (cb * 128 + 128 <= a.inter);
+    c.left = valid ? a.inter - c.col : 0;
     c.sg = c.su = 1.0f;
     if constexpr (CACHE) {
       const uint8_t* src = static_cast<const uint8_t*>(a.x) + (int64_t)c.row * a.ldx + c.col;
-      uint2 g, u;
-      if (c.full) {
-        const u32x2 gv = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(src));
-        const u32x2 uv = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(src + a.inter));
-        g = make_uint2(gv[0], gv[1]);
-        u = make_uint2(uv[0], uv[1]);
-      } else {
-        g = load8_codes_masked(src, c.nvalid);
-        u = load8_codes_masked(src + a.inter, c.nvalid);
-      }
+      const uint2 g = ld_codes8(src, c.left, a.vec), u = ld_codes8(src + a.inter, c.left, a.vec);
       c.g = make_uint4(g.x, g.y, 0, 0);
       c.u = make_uint4(u.x, u.y, 0, 0);
-      if (c.valid) {
+      if (c.left > 0) {
         const float* s = a.xscales + (int64_t)c.row * (2 * a.nb) + cb;
         c.sg = s[0];
         c.su = s[a.nb];
       }
     } else {
       const uint16_t* src = static_cast<const uint16_t*>(a.x) + (int64_t)c.row * a.ldx + c.col;
-      c.g = c.full ? ld_stream16(src) : load8_masked(src, c.nvalid);
-      c.u = c.full ? ld_stream16(src + a.inter) : load8_masked(src + a.inter, c.nvalid);
+      c.g = ld_bf16x8(src, c.left, a.vec);
+      c.u = ld_bf16x8(src + a.inter, c.left, a.vec);
     }
-    const uint16_t* dsrc = a.dy + (int64_t)c.row * a.lddy + c.col;
-    c.d = c.full ? ld_stream16(dsrc) : load8_masked(dsrc, c.nvalid);
+    c.d = ld_bf16x8(a.dy + (int64_t)c.row * a.lddy + c.col, c.left, a.vec);
   };
 
   uint32_t base = wave * 4u;
@@ -170,13 +140,13 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
     }
     const uint4 cg = make_uint4(wg[0], wg[1], wg[2], wg[3]);
     const uint4 cu = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-    if (a.dx && cur.valid) {
+    if (a.dx) {
       uint16_t* dst = a.dx + (int64_t)cur.row * a.lddx + cur.col;
-      store8(dst, cg, cur.nvalid, cur.full);
-      store8(dst + a.inter, cu, cur.nvalid, cur.full);
+      st_bf16x8(dst, cg, cur.left, a.vec);
+      st_bf16x8(dst + a.inter, cu, cur.left, a.vec);
     }
-    if (a.y && cur.valid)
-      store8(a.y + (int64_t)cur.row * a.ldy + cur.col, make_uint4(wy[0], wy[1], wy[2], wy[3]), cur.nvalid, cur.full);
+    if (a.y)
+      st_bf16x8(a.y + (int64_t)cur.row * a.ldy + cur.col, make_uint4(wy[0], wy[1], wy[2], wy[3]), cur.left, a.vec);
     if constexpr (QUANT) {
       // inter is a multiple of 128: the gate chunk is tile cb of dx's row,
       // the up chunk tile nb + cb (every lane of the wave takes part)
@@ -185,12 +155,8 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
       auto quant = [&](uint4 v, uint8_t* to, float* sto) {
         const TileScale ts = tile_scale<POW2>(dpp_max16(absmax8(v)));
         const uint2 c = encode8<POW2>(v, ts);
-        if (cur.full) {
-          st_stream8(to, c);
-        } else if (cur.valid) {
-          store8_masked(to, c, cur.nvalid);
-        }
-        if (sub == 0 && cur.valid) *sto = ts.s;
+        st_codes8(to, c, cur.left, a.vec);
+        if (sub == 0 && cur.left > 0) *sto = ts.s;
       };
       quant(cg, dst, sdst);
       quant(cu, dst + a.inter, sdst + a.nb);

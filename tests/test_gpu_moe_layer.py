@@ -172,8 +172,9 @@ def test_combine_backward(ddt, ydt, tokens, topk, n, experts, hosted):
     yv[token < 0] = np.nan
     y, dout = torch.from_numpy(yv).to("cuda:0").to(ydt), torch.from_numpy(dv).to("cuda:0").to(ddt)
     rows_d, token_d = dev(row_of.astype(np.int32)), dev(token.astype(np.int32))
-    # a product of at most 24 depth: each lane's chunk sums, six shuffles, three additions
-    depth = 8 * (-(-n // 2048)) + 10
+    # additions behind one another: eight a chunk in each lane (a workgroup of at least 64 lanes goes over the row in
+    # steps of 512 columns or more), six between lanes, three between waves
+    depth = 8 * (-(-n // 512)) + 10
     for weights, mode, pad in ((w, "free", 0), (None, "pow2", 5), (w, "pow2", 8)):
         want_dy, want_dw, mag = M.combine_backward(dv, yv, row_of, weights)
         w32 = (np.ones_like(w) if weights is None else weights)
