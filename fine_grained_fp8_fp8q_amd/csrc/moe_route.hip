@@ -10,6 +10,8 @@
 //   quantized per 1x128 tile (jp-study.kr doc 258368 ¶1, tmdrlife.com
 //   wr_id=13334 ¶4: the activation gradient before the down-projections is
 //   one of the tensors that take FP8), and dw[t,j] = <dout[t], y[row]>.
+#include <type_traits>
+
 #include "chunk8.h"
 #include "fp8q_internal.h"
 #include "quant_common.h"
@@ -197,40 +199,57 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 // --------------------------------------------------------------- combine ---
 // One workgroup per token and chunk of 8 x threads columns: the rows and
 // weights of the token are wave-uniform, and the chunks of up to eight rows
-// are in flight at once.
-template <bool YF32, bool OF32>
+// are in flight at once.  A thread has eight columns side by side for a BF16
+// output, and four in each half of the chunk for a float32 one.  Bound by
+// HBM: 4096 tokens x 8 rows x 7168 (BF16) at 5.4 TB/s (97 us), the gradient
+// of a dispatch that leaves most tokens without a row (8192 x 7168 float32
+// out) at 7.1 TB/s (41 us; 64-69 us with eight columns side by side).
+template <bool YF32, bool OF32, bool VEC>
 __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y, int cap, int n, int64_t ldy,
-                               const int* __restrict__ row_of, const float* __restrict__ weights, int topk,
-                               int chunks, void* __restrict__ out, int64_t ldo, bool vec) {
+                                                      const int* __restrict__ row_of,
+                                                      const float* __restrict__ weights, int topk, int chunks,
+                                                      void* __restrict__ out, int64_t ldo) {
+  constexpr int W = OF32 ? 4 : 8, H = OF32 ? 2 : 1;  // columns of a load, loads of a row
   const int t = blockIdx.x / chunks;
-  const int col = ((blockIdx.x - t * chunks) * (int)blockDim.x + (int)threadIdx.x) * 8;
-  if (col >= n) return;
+  const int col0 = (blockIdx.x - t * chunks) * (int)blockDim.x * 8 + (int)threadIdx.x * W;
+  if (col0 >= n) return;
   const int* rows = row_of + (int64_t)t * topk;
   const float* w = weights ? weights + (int64_t)t * topk : nullptr;
-  F8 acc;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc.v[i] = 0.0f;
+  float acc[H][W] = {};
   for (int j0 = 0; j0 < topk; j0 += 8) {
-    F8 v[8];
+    Raw<YF32, W> v[8][H];
     bool has[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int r = j0 + u < topk ? rows[j0 + u] : -1;
       has[u] = (unsigned)r < (unsigned)cap;
-      if (has[u]) v[u] = ld_float8<YF32>(y, (int64_t)r * ldy + col, n - col, vec);
+      if (!has[u]) continue;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const int col = col0 + h * W * (int)blockDim.x;
+        if (VEC && h > 0 && col >= n) continue;
+        v[u][h] = ld_raw<YF32, W>(y, (int64_t)r * ldy + col, VEC ? W : n - col, VEC);
+      }
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if (!has[u]) continue;
       const float wj = w ? w[j0 + u] : 1.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc.v[i] = __builtin_fmaf(wj, v[u].v[i], acc.v[i]);
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[h][i] = __builtin_fmaf(wj, v[u][h].at(i), acc[h][i]);
     }
   }
   if constexpr (OF32) {
-    st_float8(static_cast<float*>(out) + (int64_t)t * ldo + col, acc, n - col, vec);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int col = col0 + h * W * (int)blockDim.x;
+      if (VEC && h > 0 && col >= n) continue;
+      st_float4(static_cast<float*>(out) + (int64_t)t * ldo + col, acc[h], VEC ? W : n - col, VEC);
+    }
   } else {
-    st_bf16x8(static_cast<uint16_t*>(out) + (int64_t)t * ldo + col, pack_bf16x8(acc), n - col, vec);
+    st_bf16x8(static_cast<uint16_t*>(out) + (int64_t)t * ldo + col0, pack_bf16x8(acc[0]), VEC ? W : n - col0, VEC);
   }
 }
 
@@ -250,16 +269,16 @@ struct CombineBwdArgs {
   float* scales;
   float* dweights;
   int pairs, topk, n, cap;
-  bool vec;
 };
 
 constexpr int kZeroRows = 16;  // rows looked over by one of the trailing workgroups
 
 // Workgroup p < pairs: pair p.  The pairs of a token follow one another on
 // one XCD, so its gradient row comes from HBM once and from that XCD's L2
-// for the other choices.  The workgroups behind the pairs clear the rows
-// without a pair.
-template <bool DF32, bool YF32, bool POW2>
+// for the other choices (4096 x 8 x 7168 to E4M3: 158 us with streaming loads
+// of it, 144 us, 5.4 TB/s, without).  The workgroups behind the pairs clear
+// the rows without a pair.
+template <bool DF32, bool YF32, bool POW2, bool VEC>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   __shared__ float part[4];
   const int tid = threadIdx.x;
@@ -271,8 +290,9 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
     for (; clear; clear &= clear - 1) {
       const int r = r0 + __builtin_ctzll(clear);
       for (int col = tid * 8; col < a.n; col += step) {
-        if (a.dy) st_bf16x8(a.dy + (int64_t)r * a.lddy + col, make_uint4(0, 0, 0, 0), a.n - col, a.vec);
-        if (a.codes) st_codes8(a.codes + (int64_t)r * a.ldc + col, make_uint2(0, 0), a.n - col, a.vec);
+        const int left = VEC ? 8 : a.n - col;
+        if (a.dy) st_bf16x8(a.dy + (int64_t)r * a.lddy + col, make_uint4(0, 0, 0, 0), left, VEC);
+        if (a.codes) st_codes8(a.codes + (int64_t)r * a.ldc + col, make_uint2(0, 0), left, VEC);
       }
       if (a.codes)
         for (int j = tid; j < nb; j += (int)blockDim.x) a.scales[(int64_t)r * nb + j] = 0.0f;
@@ -292,25 +312,28 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   const float w = a.weights ? a.weights[p] : 1.0f;
   float dot = 0.0f;
   for (int c0 = 0; c0 < a.n; c0 += step) {
-    const int col = c0 + tid * 8, left = a.n - col;
-    const bool in = left > 0;
-    F8 g = {}, v = {};
+    const int col = c0 + tid * 8, left = VEC ? 8 : a.n - col;
+    const bool in = col < a.n;
+    float g[8] = {};
     if (in) {
-      g = ld_float8<DF32>(a.dout, (int64_t)t * a.lddo + col, left, a.vec);
-      if (a.y) v = ld_float8<YF32>(a.y, (int64_t)row * a.ldy + col, left, a.vec);
+      const auto gr = ld_raw<DF32, 8, true>(a.dout, (int64_t)t * a.lddo + col, left, VEC);
+      Raw<YF32, 8> v = {};
+      if (a.y) v = ld_raw<YF32, 8>(a.y, (int64_t)row * a.ldy + col, left, VEC);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = gr.at(i);
+        dot = __builtin_fmaf(g[i], v.at(i), dot);
+        g[i] = w * g[i];
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(g.v[i], v.v[i], dot);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g.v[i] = w * g.v[i];
     const uint4 d = pack_bf16x8(g);
-    if (a.dy && in) st_bf16x8(a.dy + (int64_t)row * a.lddy + col, d, left, a.vec);
+    if (a.dy && in) st_bf16x8(a.dy + (int64_t)row * a.lddy + col, d, left, VEC);
     if (a.codes) {
       // a 16-lane DPP row holds one 1x128 tile; every lane takes part
       const TileScale ts = tile_scale<POW2>(dpp_max16(absmax8(d)));
       const uint2 c = encode8<POW2>(d, ts);
       if (in) {
-        st_codes8(a.codes + (int64_t)row * a.ldc + col, c, left, a.vec);
+        st_codes8(a.codes + (int64_t)row * a.ldc + col, c, left, VEC);
         if ((tid & 15) == 0) a.scales[(int64_t)row * nb + (col >> 7)] = ts.s;
       }
     }
@@ -358,34 +381,31 @@ static int row_threads(int n) {
   return threads;
 }
 
+// VEC: every row starts on a 16-byte boundary and has whole chunks, so the
+// kernels need no checks of a chunk's end (with them at every load the
+// float32 sum above takes 74 us instead of 41).
+template <class F>
+static void with_vec(bool vec, F f) {
+  if (vec) {
+    f(std::true_type{});
+  } else {
+    f(std::false_type{});
+  }
+}
+
 hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t ldy, const int* row_of,
                               const float* weights, int tokens, int topk, bool out_f32, void* out, int64_t ldo,
                               hipStream_t stream) {
-  const bool vec = n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0;
   const int items = (n + 7) / 8, threads = row_threads(n);
   const int chunks = (items + threads - 1) / threads;
   const dim3 grid((unsigned)(tokens * chunks)), block(threads);
-  if (y_f32) {
-    if (out_f32)
-      hipLaunchKernelGGL((combine_kernel<true, true>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
-    else
-      hipLaunchKernelGGL((combine_kernel<true, false>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
-  } else {
-    if (out_f32)
-      hipLaunchKernelGGL((combine_kernel<false, true>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
-    else
-      hipLaunchKernelGGL((combine_kernel<false, false>), grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo, vec);
-  }
+  with_vec(n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0, [&](auto vec) {
+    constexpr bool V = decltype(vec)::value;
+    auto kernel = y_f32 ? (out_f32 ? combine_kernel<true, true, V> : combine_kernel<true, false, V>)
+                        : (out_f32 ? combine_kernel<false, true, V> : combine_kernel<false, false, V>);
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo);
+  });
   return hipGetLastError();
-}
-
-template <bool DF32, bool YF32>
-static void launch_bwd(const CombineBwdArgs& a, int grid, bool pow2, hipStream_t stream) {
-  const dim3 block(row_threads(a.n));
-  if (pow2)
-    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, true>), dim3(grid), block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((combine_bwd_kernel<DF32, YF32, false>), dim3(grid), block, 0, stream, a);
 }
 
 hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int tokens, int n, int64_t lddo,
@@ -397,14 +417,17 @@ hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int toke
   a.dout = dout; a.lddo = lddo; a.y = y; a.ldy = ldy; a.row_of = row_of; a.weights = weights; a.token = token;
   a.dy = dy; a.lddy = lddy; a.codes = codes; a.ldc = ldc; a.scales = scales; a.dweights = dweights;
   a.pairs = tokens * topk; a.topk = topk; a.n = n; a.cap = cap;
-  a.vec = n % 8 == 0 && lddo % 8 == 0 && (!y || ldy % 8 == 0) && (!dy || lddy % 8 == 0) && (!codes || ldc % 8 == 0);
+  const bool whole = n % 8 == 0 && lddo % 8 == 0 && (!y || ldy % 8 == 0) && (!dy || lddy % 8 == 0) && (!codes || ldc % 8 == 0);
   const int zero = token && (dy || codes) ? (cap + kZeroRows - 1) / kZeroRows : 0;
-  const int grid = a.pairs + zero;
-  if (dout_f32) {
-    y_f32 ? launch_bwd<true, true>(a, grid, pow2, stream) : launch_bwd<true, false>(a, grid, pow2, stream);
-  } else {
-    y_f32 ? launch_bwd<false, true>(a, grid, pow2, stream) : launch_bwd<false, false>(a, grid, pow2, stream);
-  }
+  const dim3 grid(a.pairs + zero), block(row_threads(n));
+  with_vec(whole, [&](auto vec) {
+    constexpr bool V = decltype(vec)::value;
+    auto kernel = dout_f32 ? (y_f32 ? (pow2 ? combine_bwd_kernel<true, true, true, V> : combine_bwd_kernel<true, true, false, V>)
+                                    : (pow2 ? combine_bwd_kernel<true, false, true, V> : combine_bwd_kernel<true, false, false, V>))
+                           : (y_f32 ? (pow2 ? combine_bwd_kernel<false, true, true, V> : combine_bwd_kernel<false, true, false, V>)
+                                    : (pow2 ? combine_bwd_kernel<false, false, true, V> : combine_bwd_kernel<false, false, false, V>));
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
+  });
   return hipGetLastError();
 }
 

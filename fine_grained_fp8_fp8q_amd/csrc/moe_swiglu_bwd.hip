@@ -36,7 +36,6 @@ struct SwigluBwdArgs {
   uint16_t* y;       // null: not written
   int64_t ldy;
   int inter, nb, ntiles;
-  bool vec;
 };
 
 // Eight elements of x: BF16 (16 bytes) or E4M3 codes (8 bytes, in .x and .y)
@@ -68,7 +67,7 @@ __device__ __forceinline__ void widen8(uint4 c, float scale, float* v) {
 // of inter (lane sub: 8 gates and 8 ups), a wave four tiles a step of a
 // grid-stride loop, with the next step's loads in flight through the
 // arithmetic of this one.
-template <bool CACHE, bool QUANT, bool POW2>
+template <bool CACHE, bool QUANT, bool POW2, bool VEC>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
   const int lane = threadIdx.x & 63;
   const int grp = lane >> 4, sub = lane & 15;
@@ -87,10 +86,11 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
     const int cb = valid ? (int)(t - (uint32_t)c.row * (uint32_t)a.nb) : 0;
     c.col = cb * 128 + sub * 8;
     c.left = valid ? a.inter - c.col : 0;
+    if (VEC) c.left = c.left > 0 ? 8 : 0;  // whole chunks only
     c.sg = c.su = 1.0f;
     if constexpr (CACHE) {
       const uint8_t* src = static_cast<const uint8_t*>(a.x) + (int64_t)c.row * a.ldx + c.col;
-      const uint2 g = ld_codes8(src, c.left, a.vec), u = ld_codes8(src + a.inter, c.left, a.vec);
+      const uint2 g = ld_codes8(src, c.left, VEC), u = ld_codes8(src + a.inter, c.left, VEC);
       c.g = make_uint4(g.x, g.y, 0, 0);
       c.u = make_uint4(u.x, u.y, 0, 0);
       if (c.left > 0) {
@@ -100,10 +100,10 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
       }
     } else {
       const uint16_t* src = static_cast<const uint16_t*>(a.x) + (int64_t)c.row * a.ldx + c.col;
-      c.g = ld_bf16x8(src, c.left, a.vec);
-      c.u = ld_bf16x8(src + a.inter, c.left, a.vec);
+      c.g = ld_bf16x8(src, c.left, VEC);
+      c.u = ld_bf16x8(src + a.inter, c.left, VEC);
     }
-    c.d = ld_bf16x8(a.dy + (int64_t)c.row * a.lddy + c.col, c.left, a.vec);
+    c.d = ld_bf16x8(a.dy + (int64_t)c.row * a.lddy + c.col, c.left, VEC);
   };
 
   uint32_t base = wave * 4u;
@@ -142,11 +142,11 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
     const uint4 cu = make_uint4(wu[0], wu[1], wu[2], wu[3]);
     if (a.dx) {
       uint16_t* dst = a.dx + (int64_t)cur.row * a.lddx + cur.col;
-      st_bf16x8(dst, cg, cur.left, a.vec);
-      st_bf16x8(dst + a.inter, cu, cur.left, a.vec);
+      st_bf16x8(dst, cg, cur.left, VEC);
+      st_bf16x8(dst + a.inter, cu, cur.left, VEC);
     }
     if (a.y)
-      st_bf16x8(a.y + (int64_t)cur.row * a.ldy + cur.col, make_uint4(wy[0], wy[1], wy[2], wy[3]), cur.left, a.vec);
+      st_bf16x8(a.y + (int64_t)cur.row * a.ldy + cur.col, make_uint4(wy[0], wy[1], wy[2], wy[3]), cur.left, VEC);
     if constexpr (QUANT) {
       // inter is a multiple of 128: the gate chunk is tile cb of dx's row,
       // the up chunk tile nb + cb (every lane of the wave takes part)
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
       auto quant = [&](uint4 v, uint8_t* to, float* sto) {
         const TileScale ts = tile_scale<POW2>(dpp_max16(absmax8(v)));
         const uint2 c = encode8<POW2>(v, ts);
-        st_codes8(to, c, cur.left, a.vec);
+        st_codes8(to, c, cur.left, VEC);
         if (sub == 0 && cur.left > 0) *sto = ts.s;
       };
       quant(cg, dst, sdst);
@@ -165,21 +165,12 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
   }
 }
 
-template <bool CACHE, bool QUANT, bool POW2>
-void launch(const SwigluBwdArgs& a, hipStream_t stream) {
+template <bool CACHE, bool VEC>
+void launch(const SwigluBwdArgs& a, bool pow2, hipStream_t stream) {
   const int64_t waves = ((int64_t)a.ntiles + 3) / 4;
-  hipLaunchKernelGGL((swiglu_bwd_kernel<CACHE, QUANT, POW2>), dim3(stream_grid(waves)), dim3(256), 0, stream, a);
-}
-
-template <bool CACHE>
-void launch_form(const SwigluBwdArgs& a, bool pow2, hipStream_t stream) {
-  if (!a.codes) {
-    launch<CACHE, false, false>(a, stream);
-  } else if (pow2) {
-    launch<CACHE, true, true>(a, stream);
-  } else {
-    launch<CACHE, true, false>(a, stream);
-  }
+  auto kernel = !a.codes ? swiglu_bwd_kernel<CACHE, false, false, VEC>
+                         : pow2 ? swiglu_bwd_kernel<CACHE, true, true, VEC> : swiglu_bwd_kernel<CACHE, true, false, VEC>;
+  hipLaunchKernelGGL(kernel, dim3(stream_grid(waves)), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -192,12 +183,13 @@ hipError_t launch_swiglu_backward(const void* x, const float* xscales, int rows,
   a.x = x; a.xscales = xscales; a.ldx = ldx; a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
   a.codes = codes; a.ldc = ldc; a.scales = scales; a.y = y; a.ldy = ldy;
   a.inter = inter; a.nb = (inter + 127) / 128; a.ntiles = rows * a.nb;  // < 2^31 (checked by the entry point)
-  a.vec = inter % 8 == 0 && ldx % 8 == 0 && lddy % 8 == 0 && (!dx || lddx % 8 == 0) && (!codes || ldc % 8 == 0) &&
-          (!y || ldy % 8 == 0);
+  // VEC: whole 8-element chunks on 16-byte (codes: 8-byte) boundaries
+  const bool vec = inter % 8 == 0 && ldx % 8 == 0 && lddy % 8 == 0 && (!dx || lddx % 8 == 0) &&
+                   (!codes || ldc % 8 == 0) && (!y || ldy % 8 == 0);
   if (xscales) {
-    launch_form<true>(a, pow2, stream);
+    vec ? launch<true, true>(a, pow2, stream) : launch<true, false>(a, pow2, stream);
   } else {
-    launch_form<false>(a, pow2, stream);
+    vec ? launch<false, true>(a, pow2, stream) : launch<false, false>(a, pow2, stream);
   }
   return hipGetLastError();
 }
