@@ -200,11 +200,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 // One workgroup per token and chunk of 8 x threads columns: the rows and
 // weights of the token are wave-uniform, and the chunks of up to eight rows
 // are in flight at once.  A thread has eight columns side by side for a BF16
-// output, and four in each half of the chunk for a float32 one.  Bound by
-// HBM: 4096 tokens x 8 rows x 7168 (BF16) at 5.4 TB/s (97 us), the gradient
-// of a dispatch that leaves most tokens without a row (8192 x 7168 float32
-// out) at 7.1 TB/s (41 us; 64-69 us with eight columns side by side).
-template <bool YF32, bool OF32, bool VEC>
+// output, and four in each half of the chunk for a float32 one (stores of
+// whole lines: 54 us instead of 64-69 for 8192 x 7168).  Bound by HBM: 4096
+// tokens x 8 rows x 7168 (BF16) at 5.9 TB/s (90 us).
+template <bool YF32, bool OF32, bool VEC, bool KEEP>
 __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y, int cap, int n, int64_t ldy,
                                                       const int* __restrict__ row_of,
                                                       const float* __restrict__ weights, int topk, int chunks,
@@ -228,7 +227,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
       for (int h = 0; h < H; ++h) {
         const int col = col0 + h * W * (int)blockDim.x;
         if (VEC && h > 0 && col >= n) continue;
-        v[u][h] = ld_raw<YF32, W>(y, (int64_t)r * ldy + col, VEC ? W : n - col, VEC);
+        v[u][h] = ld_raw<YF32, W, KEEP>(y, (int64_t)r * ldy + col, VEC ? W : n - col, VEC);
       }
     }
 #pragma unroll
@@ -382,11 +381,11 @@ static int row_threads(int n) {
 }
 
 // VEC: every row starts on a 16-byte boundary and has whole chunks, so the
-// kernels need no checks of a chunk's end (with them at every load the
-// float32 sum above takes 74 us instead of 41).
+// kernels need no checks of a chunk's end (with them at every load the two
+// sums above take 97 and 74 us).
 template <class F>
-static void with_vec(bool vec, F f) {
-  if (vec) {
+static void with_flag(bool flag, F f) {
+  if (flag) {
     f(std::true_type{});
   } else {
     f(std::false_type{});
@@ -399,11 +398,19 @@ hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t
   const int items = (n + 7) / 8, threads = row_threads(n);
   const int chunks = (items + threads - 1) / threads;
   const dim3 grid((unsigned)(tokens * chunks)), block(threads);
-  with_vec(n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0, [&](auto vec) {
-    constexpr bool V = decltype(vec)::value;
-    auto kernel = y_f32 ? (out_f32 ? combine_kernel<true, true, V> : combine_kernel<true, false, V>)
-                        : (out_f32 ? combine_kernel<false, true, V> : combine_kernel<false, false, V>);
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo);
+  // Rows that a GEMM has just written are in the 256 MB Infinity Cache as
+  // long as all of them fit beside the output: plain loads find them there
+  // (87 MB of rows for 8192 tokens: 27 us against 34 with streaming loads,
+  // float32 out 38 against 52).  More rows are streamed (448 MB: 88 us against 95;
+  // 112 MB: 23 against 25).
+  const bool keep = (int64_t)cap * ldy * (y_f32 ? 4 : 2) <= (int64_t)96 << 20;
+  with_flag(n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0, [&](auto vec) {
+    with_flag(keep, [&](auto kept) {
+      constexpr bool V = decltype(vec)::value, K = decltype(kept)::value;
+      auto kernel = y_f32 ? (out_f32 ? combine_kernel<true, true, V, K> : combine_kernel<true, false, V, K>)
+                          : (out_f32 ? combine_kernel<false, true, V, K> : combine_kernel<false, false, V, K>);
+      hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo);
+    });
   });
   return hipGetLastError();
 }
@@ -420,7 +427,7 @@ hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int toke
   const bool whole = n % 8 == 0 && lddo % 8 == 0 && (!y || ldy % 8 == 0) && (!dy || lddy % 8 == 0) && (!codes || ldc % 8 == 0);
   const int zero = token && (dy || codes) ? (cap + kZeroRows - 1) / kZeroRows : 0;
   const dim3 grid(a.pairs + zero), block(row_threads(n));
-  with_vec(whole, [&](auto vec) {
+  with_flag(whole, [&](auto vec) {
     constexpr bool V = decltype(vec)::value;
     auto kernel = dout_f32 ? (y_f32 ? (pow2 ? combine_bwd_kernel<true, true, true, V> : combine_bwd_kernel<true, true, false, V>)
                                     : (pow2 ? combine_bwd_kernel<true, false, true, V> : combine_bwd_kernel<true, false, false, V>))
