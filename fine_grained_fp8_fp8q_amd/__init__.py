@@ -698,37 +698,42 @@ def grouped_wgrad(dy_t, dy_scales, x_t, x_scales, offsets, out=None, acc="fp32")
     align=128).  An empty group gives zeros.
     """
     torch = _torch()
-    _contig_codes(dy_t, "dy_t")
-    _contig_codes(x_t, "x_t")
-    _contig_f32(dy_scales, "dy_scales")
-    _contig_f32(x_scales, "x_scales")
-    _need(offsets, torch.int32, "offsets")
-    if offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
-        raise ValueError("offsets must be a contiguous int32 [G+1] tensor")
-    if dy_t.dim() != 2 or x_t.dim() != 2 or dy_t.shape[1] != x_t.shape[1]:
+    u8, f32 = (torch.uint8,), (torch.float32,)
+    nout, cap, ld0, dy_p = _rows_of(dy_t, "dy_t", u8)
+    kin, xcap, ld1, x_p = _rows_of(x_t, "x_t", u8)
+    if cap != xcap:
         raise ValueError("operand shapes do not match")
-    nout, cap = dy_t.shape
-    kin = x_t.shape[0]
     if cap % 128:
         raise ValueError("the token axis must be a multiple of 128")
-    if tuple(dy_scales.shape) != (nout, cap // 128) or tuple(x_scales.shape) != (kin, cap // 128):
+    sr, sc, ld2, dys_p = _rows_of(dy_scales, "dy_scales", f32)
+    xr, xc, ld3, xs_p = _rows_of(x_scales, "x_scales", f32)
+    nb = cap // 128
+    if (sr, sc, xr, xc) != (nout, nb, kin, nb):
         raise ValueError("scales must be [rows of the codes, tokens/128]")
+    if cap and (ld0, ld1, ld2, ld3) != (cap, cap, nb, nb):
+        raise ValueError("codes and scales must be contiguous")
+    if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.dim() != 1 or not offsets.is_contiguous() or \
+            not offsets.numel():
+        _need(offsets, torch.int32, "offsets")
+        raise ValueError("offsets must be a contiguous int32 [G+1] tensor")
     g = offsets.numel() - 1
+    ldw = max(kin, 1)
     if out is None:
-        dw = torch.empty((g, nout, kin), dtype=torch.float32, device=dy_t.device)
+        dw = dy_scales.new_empty((g, nout, kin))
     else:
         dw = out
         _need(dw, torch.float32, "out")
         if tuple(dw.shape) != (g, nout, kin):
             raise ValueError(f"out must be [{g}, {nout}, {kin}], got {tuple(dw.shape)}")
-        if dw.numel() and (dw.stride(2) != 1 or dw.stride(1) < kin or (g > 1 and dw.stride(0) != nout * dw.stride(1))):
-            raise ValueError("out must have contiguous rows and matrices that follow one another")
+        if dw.numel():
+            ldw = dw.stride(1) if nout > 1 else dw.stride(0) if g > 1 else kin
+            if (kin > 1 and dw.stride(2) != 1) or ldw < kin or (g > 1 and dw.stride(0) != nout * ldw):
+                raise ValueError("out must have contiguous rows and matrices that follow one another")
     dev = _one_device(dy_t, dy_scales, x_t, x_scales, offsets, dw)
-    args = (_addr(dy_t), _addr(dy_scales), _addr(x_t), _addr(x_scales), _addr(offsets), g, cap, nout, kin)
-    tail = (_addr(dw), dw.stride(1) if dw.numel() else max(kin, 1))
     code = _acc_code(acc)
+    args = (dy_p, dys_p, x_p, xs_p, offsets.data_ptr(), g, cap, nout, kin)
     if code == ACC_FP32:
-        _call(dev, "fp8q_grouped_wgrad", *args, *tail)
+        _call(dev, "fp8q_grouped_wgrad", *args, _addr(dw), ldw)
     else:
-        _call(dev, "fp8q_grouped_wgrad_ex", *args, code, *tail)
+        _call(dev, "fp8q_grouped_wgrad_ex", *args, code, _addr(dw), ldw)
     return dw

@@ -303,12 +303,12 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   const int per = a.pairs >> 3, rem = a.pairs & 7;
   const int p = xcd * per + min(xcd, rem) + idx;
   const int row = a.row_of[p];
+  const float w = a.weights ? a.weights[p] : 1.0f;
   if ((unsigned)row >= (unsigned)a.cap) {
     if (tid == 0 && a.dweights) a.dweights[p] = 0.0f;
     return;
   }
   const int t = (int)((unsigned)p / (unsigned)a.topk);
-  const float w = a.weights ? a.weights[p] : 1.0f;
   float dot = 0.0f;
   for (int c0 = 0; c0 < a.n; c0 += step) {
     const int col = c0 + tid * 8, left = VEC ? 8 : a.n - col;
@@ -371,11 +371,12 @@ hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, i
 }
 
 // Threads of a workgroup that goes over a row of n columns, eight a thread:
-// 256, 128 or 64, whichever leaves the fewest idle (7168 columns: 7 x 128).
+// of 64, 128, 192 and 256 the one that leaves the fewest idle, the largest of
+// equals (7168 columns: 7 x 128; 1030: 192).
 static int row_threads(int n) {
   const int items = (n + 7) / 8;
   int threads = 256;
-  for (int c = 128; c >= 64; c >>= 1)
+  for (int c = 192; c >= 64; c -= 64)
     if ((items + c - 1) / c * c < (items + threads - 1) / threads * threads) threads = c;
   return threads;
 }

@@ -357,7 +357,8 @@ fp8q_status fp8q_swiglu_quantize(const void* x_bf16, int64_t rows, int64_t inter
  * G) bytes (0 for a few thousand pairs: then it may be NULL), used until the
  * call's work is done; calls that may run at the same time need one each.
  * A missing or small workspace gives FP8Q_ERR_INVALID_ARG.  G <= 512 and
- * tokens * topk + G * align < 2^31, else FP8Q_ERR_SHAPE. */
+ * tokens * topk + G * align < 2^31, else FP8Q_ERR_SHAPE.  With G = 0 nothing
+ * is written. */
 int64_t fp8q_moe_sort_workspace(int64_t tokens, int64_t topk, int32_t G);
 fp8q_status fp8q_moe_sort(const void* experts, int index_dtype, int64_t tokens, int64_t topk, int64_t ld_experts,
                           int64_t first_expert, int32_t G, int32_t align, int64_t rows_cap,

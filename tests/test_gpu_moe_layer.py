@@ -95,6 +95,36 @@ def test_sort_of_a_column_slice():
         fp8q.moe_sort(wide, 64, align=128, rows_cap=100)
 
 
+def check_sort_by_rules(experts, first, groups, align, cap):
+    """The same conditions without the oracle's loops, for many pairs: every hosted pair has a row of its group, the
+    rows of a group are its pairs in ascending order, and everything else is -1."""
+    offsets, token, row_of = (host(v).astype(np.int64) for v in fp8q.moe_sort(dev(experts), groups, first=first, align=align, rows_cap=cap))
+    flat, topk = experts.reshape(-1), experts.shape[1]
+    counts = np.array([(flat == first + g).sum() for g in range(groups)])
+    starts = np.concatenate([[0], np.cumsum(-(-counts // align) * align)])
+    assert np.array_equal(offsets, np.minimum(starts, cap))
+    want_token, want_row = np.full(cap, -1), np.full(flat.size, -1)
+    for g in range(groups):
+        p = np.flatnonzero(flat == first + g)
+        rows = starts[g] + np.arange(p.size)
+        fits = rows < cap
+        want_row[p[fits]] = rows[fits]
+        want_token[rows[fits]] = p[fits] // topk
+    assert np.array_equal(row_of.reshape(-1), want_row) and np.array_equal(token, want_token)
+
+
+@pytest.mark.parametrize("tokens,topk,experts,first,groups,align", [
+    (150001, 8, 64, 0, 64, 128), (400003, 3, 9, 2, 5, 1), (262145, 4, 512, 0, 512, 16), (1100000, 1, 3, 0, 3, 1), (2048, 2, 4, 0, 4, 1),
+    (2049, 2, 4, 0, 4, 1)])
+def test_sort_of_many_pairs(tokens, topk, experts, first, groups, align):
+    """More pairs than the kernel keeps in registers between its passes (above a million), and both sides of the
+    size from which more than one workgroup counts."""
+    e = np.random.default_rng(tokens).integers(0, experts, size=(tokens, topk))
+    cap = -(-(tokens * topk + groups * align) // align) * align
+    check_sort_by_rules(e, first, groups, align, cap)
+    check_sort_by_rules(e, first, groups, align, cap // 3 // align * align)
+
+
 # --------------------------------------------------------------- combine ----
 
 COMBINE = [(1, 8, 7168, 256, 256), (5, 1, 8, 4, 4), (3, 3, 1, 4, 2), (17, 6, 1030, 32, 16), (64, 8, 2048, 8, 8), (33, 12, 513, 20, 20),
@@ -227,11 +257,10 @@ def test_combine_backward_empty():
 
 # ------------------------------------------------------- SwiGLU backward ----
 
-@pytest.mark.parametrize("cache", [None, "free", "pow2"])
-@pytest.mark.parametrize("rows,inter", [(1, 128), (3, 256), (130, 128), (77, 1024), (2, 2048), (50, 7), (1, 1), (19, 1000), (33, 136)])
-def test_swiglu_backward(cache, rows, inter):
-    if cache and inter % 128:
-        pytest.skip("the FP8 cache has whole tiles")
+# (the FP8 cache has whole tiles)
+@pytest.mark.parametrize("rows,inter,cache", [(r, i, c) for r, i in ((1, 128), (3, 256), (130, 128), (77, 1024), (2, 2048)) for c in (None, "free", "pow2")] +
+                         [(50, 7, None), (1, 1, None), (19, 1000, None), (33, 136, None)])
+def test_swiglu_backward(rows, inter, cache):
     r = np.random.default_rng(rows * inter)
     xb, dyb = bf16(r, (rows, 2 * inter), 3.0), bf16(r, (rows, inter))
     if cache:
@@ -300,7 +329,8 @@ def token_operand(r, width, cap, real, mode, std=1.0):
 
 @pytest.mark.parametrize("acc,mode", [("fp32", "free"), ("fp32", "pow2"), ("fp32_pow2", "pow2"), ("fp8_mfma", "free"), ("fp8_mfma_scaled", "pow2")])
 @pytest.mark.parametrize("nout,kin,sizes", [(1, 1, [5]), (40, 72, [0, 130, 0, 1]), (256, 256, [128, 256, 384]), (300, 260, [700, 0, 65]),
-                                            (257, 225, [0, 0]), (512, 448, [1, 128, 129, 1000]), (3, 600, [640] * 9)])
+                                            (257, 225, [0, 0]), (512, 448, [1, 128, 129, 1000]), (3, 600, [640] * 9),
+                                            (2000, 4100, [700, 400])])  # (enough 256 x 256 tiles, and tokens, for the large shape)
 def test_grouped_wgrad(acc, mode, nout, kin, sizes):
     r = np.random.default_rng(nout)
     padded = [-(-s // 128) * 128 for s in sizes]
@@ -462,6 +492,52 @@ def test_layer_captured_and_replayed():
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(out, want)):
             assert torch.equal(a, b), (seed, i)
+
+
+# ---------------------------------------------------------- large offsets ----
+
+def test_rows_past_four_gigabytes():
+    """Row offsets that pass 2^31 elements and 2^32 bytes, through the sum, its gradient and SwiGLU's: rows near the
+    end against a small call on copies of the same rows, bit for bit."""
+    cap, n, tokens = 310_000, 7168, 64
+    g = torch.Generator(device="cuda:0").manual_seed(5)
+    y = torch.empty((cap, n), dtype=torch.bfloat16, device="cuda:0")
+    used = torch.cat([torch.arange(cap - 96, cap), torch.arange(32)]).to("cuda:0")
+    some = torch.randn((used.numel(), n), generator=g, device="cuda:0").bfloat16()
+    y[used] = some
+    small = torch.randperm(used.numel(), generator=g, device="cuda:0").view(tokens, 2).int()
+    rows = used[small.long()].int()
+    w = torch.rand((tokens, 2), generator=g, device="cuda:0")
+    dout = torch.randn((tokens, n), generator=g, device="cuda:0").bfloat16()
+    for odt in (torch.bfloat16, torch.float32):
+        assert torch.equal(fp8q.moe_combine(y, rows, w, out_dtype=odt), fp8q.moe_combine(some, small, w, out_dtype=odt))
+    a = fp8q.moe_combine_backward(dout, y, rows, w, quantize=True)
+    b = fp8q.moe_combine_backward(dout, some, small, w, quantize=True)
+    assert torch.equal(a[0][used], b[0]) and torch.equal(a[1][used], b[1]) and torch.equal(a[2][used], b[2]) and torch.equal(a[3], b[3])
+    del a
+    # 310,000 rows of 3584 gates and 3584 ups
+    dy = torch.empty((cap, n // 2), dtype=torch.bfloat16, device="cuda:0")
+    dys = torch.randn((used.numel(), n // 2), generator=g, device="cuda:0").bfloat16()
+    dy[used] = dys
+    a, b = fp8q.swiglu_backward(y, dy, want_y=True), fp8q.swiglu_backward(some, dys, want_y=True)
+    assert torch.equal(a[0][used], b[0]) and torch.equal(a[1][used], b[1])
+
+
+def test_grouped_wgrad_past_four_gigabytes():
+    """80 gradients of 4096 x 4096: the last ones' offsets pass 2^32 bytes."""
+    r = np.random.default_rng(6)
+    groups, n = 80, 4096
+    offsets = np.minimum(np.arange(groups + 1) * 128, 256).astype(np.int32)
+    offsets[-2:] = [256, 384]
+    dy_c, dy_s = token_operand(r, n, 384, np.ones(384, bool), "free")
+    d = [dev(v) for v in (dy_c, dy_s, dy_c, dy_s, offsets)]
+    out = torch.full((groups, n, n), 3.0, device="cuda:0")
+    fp8q.grouped_wgrad(*d, out=out)
+    for g in (0, 1, groups - 1):
+        a, b = int(offsets[g]), int(offsets[g + 1])
+        c, s = d[0][:, a:b].contiguous(), d[1][:, a // 128:b // 128].contiguous()
+        assert torch.equal(out[g], fp8q.wgrad(c, s, c, s)), g
+    assert not out[2:-1].any()
 
 
 def test_large_sorts_on_two_streams_and_in_two_graphs():

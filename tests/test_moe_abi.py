@@ -114,6 +114,35 @@ def test_binding_refuses_host_tensors():
         fp8q.grouped_wgrad(c, s, c, s, torch.zeros(2, dtype=torch.int32))
 
 
+def test_calls_run_on_the_tensors_own_device(monkeypatch):
+    """With another device current the call is made under the tensors' device and on that device's stream."""
+    seen, current = [], [0]
+
+    class On:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            current.append(self.dev.index)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    class Lib:
+        @staticmethod
+        def fp8q_moe_combine(*args):
+            seen.append((current[-1], args))
+            return 0
+
+    monkeypatch.setattr(fp8q, "_lib", Lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(fp8q, "_raw_stream", lambda dev: 1000 + dev.index)
+    fp8q._call(torch.device("cuda:0"), "fp8q_moe_combine", 7)
+    fp8q._call(torch.device("cuda:1"), "fp8q_moe_combine", 8)
+    assert seen == [(0, (7, 1000)), (1, (8, 1001))] and current == [0]
+
+
 def test_host_code_under_sanitizers(tmp_path):
     gxx = shutil.which("g++")
     if gxx is None or not os.path.isdir(os.path.join(HIP_INCLUDE, "hip")):
