@@ -109,7 +109,7 @@ fp8q_status fp8q_swiglu_backward(const void* x, const float* x_scales, int64_t r
       (y_bf16 && ld_y < inter))
     return FP8Q_ERR_SHAPE;
   if ((x_scales || dx_codes) && inter % 128) return FP8Q_ERR_SHAPE;
-  if (rows * ((inter + 127) / 128) > kMaxDim) return FP8Q_ERR_SHAPE;
+  if (rows * ((inter + 127) / 128) >= 16 * (kMaxGroups - 1)) return FP8Q_ERR_SHAPE;  // 16 tiles a workgroup
   if (!aligned16(x) || !aligned16(x_scales) || !aligned16(dy_bf16) || !aligned16(dx_bf16) || !aligned16(dx_codes) ||
       !aligned16(dx_scales) || !aligned16(y_bf16))
     return FP8Q_ERR_ALIGN;

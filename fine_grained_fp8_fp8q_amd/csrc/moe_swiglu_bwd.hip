@@ -19,7 +19,6 @@
 namespace fp8q {
 namespace {
 
-typedef __bf16 sb_v2bf __attribute__((ext_vector_type(2)));
 typedef float sb_v2f __attribute__((ext_vector_type(2)));
 
 struct SwigluBwdArgs {
@@ -64,113 +63,84 @@ __device__ __forceinline__ void widen8(uint4 c, float scale, float* v) {
 }
 
 // As in the forward kernel, a 16-lane DPP row owns one tile of 128 columns
-// of inter (lane sub: 8 gates and 8 ups), a wave four tiles a step of a
-// grid-stride loop, with the next step's loads in flight through the
-// arithmetic of this one.
+// of inter (lane sub: 8 gates and 8 ups), a wave four tiles that follow one
+// another.  One pass, four tiles a wave: 32768 x 2048 from the cache with y
+// takes 107 us (6.3 TB/s); a grid of 2048 workgroups that loop with the next
+// tiles' loads in flight takes 124.
 template <bool CACHE, bool QUANT, bool POW2, bool VEC>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
   const int lane = threadIdx.x & 63;
-  const int grp = lane >> 4, sub = lane & 15;
-  const uint32_t wave = (blockIdx.x * 256u + threadIdx.x) >> 6;
-  const uint32_t step = gridDim.x * 16u;
+  const int sub = lane & 15;
+  const uint32_t t = ((blockIdx.x * 256u + threadIdx.x) >> 6) * 4u + (uint32_t)(lane >> 4);
+  const bool valid = t < (uint32_t)a.ntiles;
+  const int row = valid ? (int)(t / (uint32_t)a.nb) : 0;
+  const int cb = valid ? (int)(t - (uint32_t)row * (uint32_t)a.nb) : 0;
+  const int col = cb * 128 + sub * 8;
+  int left = valid ? a.inter - col : 0;  // columns of inter from col on (0: no tile)
+  if (VEC) left = left > 0 ? 8 : 0;      // whole chunks only
 
-  struct Chunk {
-    uint4 g, u, d;
-    float sg, su;
-    int row, col, left;  // left: columns of inter from col on (0: no tile)
-  };
-  auto fetch = [&](uint32_t base, Chunk& c) {
-    const uint32_t t = base + (uint32_t)grp;
-    const bool valid = t < (uint32_t)a.ntiles;
-    c.row = valid ? (int)(t / (uint32_t)a.nb) : 0;
-    const int cb = valid ? (int)(t - (uint32_t)c.row * (uint32_t)a.nb) : 0;
-    c.col = cb * 128 + sub * 8;
-    c.left = valid ? a.inter - c.col : 0;
-    if (VEC) c.left = c.left > 0 ? 8 : 0;  // whole chunks only
-    c.sg = c.su = 1.0f;
-    if constexpr (CACHE) {
-      const uint8_t* src = static_cast<const uint8_t*>(a.x) + (int64_t)c.row * a.ldx + c.col;
-      const uint2 g = ld_codes8(src, c.left, VEC), u = ld_codes8(src + a.inter, c.left, VEC);
-      c.g = make_uint4(g.x, g.y, 0, 0);
-      c.u = make_uint4(u.x, u.y, 0, 0);
-      if (c.left > 0) {
-        const float* s = a.xscales + (int64_t)c.row * (2 * a.nb) + cb;
-        c.sg = s[0];
-        c.su = s[a.nb];
-      }
-    } else {
-      const uint16_t* src = static_cast<const uint16_t*>(a.x) + (int64_t)c.row * a.ldx + c.col;
-      c.g = ld_bf16x8(src, c.left, VEC);
-      c.u = ld_bf16x8(src + a.inter, c.left, VEC);
+  uint4 cg, cu;
+  float sg = 1.0f, su = 1.0f;
+  if constexpr (CACHE) {
+    const uint8_t* src = static_cast<const uint8_t*>(a.x) + (int64_t)row * a.ldx + col;
+    const uint2 gc = ld_codes8(src, left, VEC), uc = ld_codes8(src + a.inter, left, VEC);
+    cg = make_uint4(gc.x, gc.y, 0, 0);
+    cu = make_uint4(uc.x, uc.y, 0, 0);
+    if (left > 0) {
+      const float* s = a.xscales + (int64_t)row * (2 * a.nb) + cb;
+      sg = s[0];
+      su = s[a.nb];
     }
-    c.d = ld_bf16x8(a.dy + (int64_t)c.row * a.lddy + c.col, c.left, VEC);
-  };
+  } else {
+    const uint16_t* src = static_cast<const uint16_t*>(a.x) + (int64_t)row * a.ldx + col;
+    cg = ld_bf16x8(src, left, VEC);
+    cu = ld_bf16x8(src + a.inter, left, VEC);
+  }
+  const uint4 cd = ld_bf16x8(a.dy + (int64_t)row * a.lddy + col, left, VEC);
 
-  uint32_t base = wave * 4u;
-  if (base >= (uint32_t)a.ntiles) return;  // (wave-uniform)
-  Chunk cur;
-  fetch(base, cur);
-  for (; base < (uint32_t)a.ntiles; base += step) {
-    Chunk nxt = cur;
-    const uint32_t nbase = base + step;
-    if (nbase < (uint32_t)a.ntiles) fetch(nbase, nxt);  // (wave-uniform)
-    float g[8], u[8], d[8];
-    widen8<CACHE>(cur.g, cur.sg, g);
-    widen8<CACHE>(cur.u, cur.su, u);
-    widen8<false>(cur.d, 1.0f, d);
-    uint32_t wg[4], wu[4], wy[4];
+  float g[8], u[8], d[8], dg[8], du[8], y[8];
+  widen8<CACHE>(cg, sg, g);
+  widen8<CACHE>(cu, su, u);
+  widen8<false>(cd, 1.0f, d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float dg[2], du[2], yy[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = 2 * i + h;
-        const float t = exp_nonpos(-__builtin_fabsf(g[k]));
-        const float r = __builtin_amdgcn_rcpf(1.0f + t);
-        const float tr = t * r;
-        const float s = g[k] >= 0.0f ? r : tr;
-        const float silu = g[k] * s;
-        yy[h] = silu * u[k];
-        du[h] = d[k] * silu;
-        dg[h] = (d[k] * u[k]) * __builtin_fmaf(silu, g[k] >= 0.0f ? tr : r, s);
-      }
-      wg[i] = __builtin_bit_cast(uint32_t, sb_v2bf{(__bf16)dg[0], (__bf16)dg[1]});
-      wu[i] = __builtin_bit_cast(uint32_t, sb_v2bf{(__bf16)du[0], (__bf16)du[1]});
-      wy[i] = __builtin_bit_cast(uint32_t, sb_v2bf{(__bf16)yy[0], (__bf16)yy[1]});
-    }
-    const uint4 cg = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-    const uint4 cu = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-    if (a.dx) {
-      uint16_t* dst = a.dx + (int64_t)cur.row * a.lddx + cur.col;
-      st_bf16x8(dst, cg, cur.left, VEC);
-      st_bf16x8(dst + a.inter, cu, cur.left, VEC);
-    }
-    if (a.y)
-      st_bf16x8(a.y + (int64_t)cur.row * a.ldy + cur.col, make_uint4(wy[0], wy[1], wy[2], wy[3]), cur.left, VEC);
-    if constexpr (QUANT) {
-      // inter is a multiple of 128: the gate chunk is tile cb of dx's row,
-      // the up chunk tile nb + cb (every lane of the wave takes part)
-      uint8_t* dst = a.codes + (int64_t)cur.row * a.ldc + cur.col;
-      float* sdst = a.scales + (int64_t)cur.row * (2 * a.nb) + (cur.col >> 7);
-      auto quant = [&](uint4 v, uint8_t* to, float* sto) {
-        const TileScale ts = tile_scale<POW2>(dpp_max16(absmax8(v)));
-        const uint2 c = encode8<POW2>(v, ts);
-        st_codes8(to, c, cur.left, VEC);
-        if (sub == 0 && cur.left > 0) *sto = ts.s;
-      };
-      quant(cg, dst, sdst);
-      quant(cu, dst + a.inter, sdst + a.nb);
-    }
-    cur = nxt;
+  for (int k = 0; k < 8; ++k) {
+    const float e = exp_nonpos(-__builtin_fabsf(g[k]));
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    const float er = e * r;
+    const float s = g[k] >= 0.0f ? r : er;
+    const float silu = g[k] * s;
+    y[k] = silu * u[k];
+    du[k] = d[k] * silu;
+    dg[k] = (d[k] * u[k]) * __builtin_fmaf(silu, g[k] >= 0.0f ? er : r, s);
+  }
+  const uint4 og = pack_bf16x8(dg), ou = pack_bf16x8(du);
+  if (a.dx) {
+    uint16_t* dst = a.dx + (int64_t)row * a.lddx + col;
+    st_bf16x8(dst, og, left, VEC);
+    st_bf16x8(dst + a.inter, ou, left, VEC);
+  }
+  if (a.y) st_bf16x8(a.y + (int64_t)row * a.ldy + col, pack_bf16x8(y), left, VEC);
+  if constexpr (QUANT) {
+    // inter is a multiple of 128: the gate chunk is tile cb of dx's row, the
+    // up chunk tile nb + cb (every lane of the wave takes part)
+    uint8_t* dst = a.codes + (int64_t)row * a.ldc + col;
+    float* sdst = a.scales + (int64_t)row * (2 * a.nb) + cb;
+    auto quant = [&](uint4 v, uint8_t* to, float* sto) {
+      const TileScale ts = tile_scale<POW2>(dpp_max16(absmax8(v)));
+      st_codes8(to, encode8<POW2>(v, ts), left, VEC);
+      if (sub == 0 && left > 0) *sto = ts.s;
+    };
+    quant(og, dst, sdst);
+    quant(ou, dst + a.inter, sdst + a.nb);
   }
 }
 
 template <bool CACHE, bool VEC>
 void launch(const SwigluBwdArgs& a, bool pow2, hipStream_t stream) {
-  const int64_t waves = ((int64_t)a.ntiles + 3) / 4;
+  const int grid = (int)(((int64_t)a.ntiles + 15) / 16);  // < 2^24
   auto kernel = !a.codes ? swiglu_bwd_kernel<CACHE, false, false, VEC>
                          : pow2 ? swiglu_bwd_kernel<CACHE, true, true, VEC> : swiglu_bwd_kernel<CACHE, true, false, VEC>;
-  hipLaunchKernelGGL(kernel, dim3(stream_grid(waves)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -182,7 +152,7 @@ hipError_t launch_swiglu_backward(const void* x, const float* xscales, int rows,
   SwigluBwdArgs a{};
   a.x = x; a.xscales = xscales; a.ldx = ldx; a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
   a.codes = codes; a.ldc = ldc; a.scales = scales; a.y = y; a.ldy = ldy;
-  a.inter = inter; a.nb = (inter + 127) / 128; a.ntiles = rows * a.nb;  // < 2^31 (checked by the entry point)
+  a.inter = inter; a.nb = (inter + 127) / 128; a.ntiles = rows * a.nb;  // < 2^28 (checked by the entry point)
   // VEC: whole 8-element chunks on 16-byte (codes: 8-byte) boundaries
   const bool vec = inter % 8 == 0 && ldx % 8 == 0 && lddy % 8 == 0 && (!dx || lddx % 8 == 0) &&
                    (!codes || ldc % 8 == 0) && (!y || ldy % 8 == 0);

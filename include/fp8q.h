@@ -421,7 +421,8 @@ fp8q_status fp8q_moe_combine_backward(const void* dout, int dout_dtype, int64_t 
  * [rows, ld_y >= inter] (for the down-projection's weight gradient) are each
  * written where the pointer is not NULL; one at least must be given.  Inputs
  * must be finite, and every dy * u and every output below the largest finite
- * float32 and BF16 value. */
+ * float32 and BF16 value.  rows * ceil(inter/128) < 2^28 - 16, else
+ * FP8Q_ERR_SHAPE. */
 fp8q_status fp8q_swiglu_backward(const void* x, const float* x_scales, int64_t rows, int64_t inter, int64_t ld_x,
                                  const void* dy_bf16, int64_t ld_dy, void* dx_bf16, int64_t ld_dx,
                                  int scale_mode, uint8_t* dx_codes, int64_t ld_codes, float* dx_scales,
