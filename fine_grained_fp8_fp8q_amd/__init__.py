@@ -484,6 +484,8 @@ def _one_device(first, *others):
 
 
 def _raw_stream(dev):
+    """Handle of the current stream of dev; asked for without making a
+    torch.cuda.Stream of it (1.8 us) where torch has the call for that."""
     torch = _torch()
     get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return get(dev.index) if get else torch.cuda.current_stream(dev).cuda_stream

@@ -129,8 +129,9 @@ fp8q_status fp8q_grouped_wgrad_ex(const uint8_t* dy_t, const float* dy_scales, c
   if (G == 0 || Nout == 0 || Kin == 0) return FP8Q_OK;
   if (!offsets) return FP8Q_ERR_INVALID_ARG;
   if (fp8q_status st = check_gemm_common(rows_cap, FP8Q_OUT_F32, dw, ld_dw, Kin)) return st;
-  // one workgroup of 256 threads per 128 x 128 outputs
-  const int64_t tiles = ((Nout + 127) / 128) * ((Kin + 127) / 128);
+  // one workgroup of 256 threads per 128 x 128 outputs, and eight regions of
+  // whole tiles: at most seven rows and columns of them more
+  const int64_t tiles = ((Nout + 127) / 128 + 7) * ((Kin + 127) / 128 + 7);
   if (Nout * rows_cap >= kMaxOperandBytes || Kin * rows_cap >= kMaxOperandBytes || tiles >= kMaxGroups ||
       tiles * G >= kMaxGroups)
     return FP8Q_ERR_SHAPE;

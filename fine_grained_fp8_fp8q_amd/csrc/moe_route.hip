@@ -20,6 +20,12 @@ namespace fp8q {
 namespace {
 
 // ------------------------------------------------------------------ sort ---
+// Bound by latency: 16384 x 8 pairs are 1.6 MB in and out, and the two
+// launches take 3.1 and 6.1 us (a single workgroup, for a few thousand pairs
+// or fewer, 4.5 us).  A count per workgroup costs the second launch a read of
+// the whole table, which is cheaper than one workgroup that goes over all
+// pairs twice from about 4096 pairs on, and unlike one pass with a running
+// total handed on it has nobody wait for another workgroup.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
 struct SortArgs {
@@ -274,9 +280,11 @@ constexpr int kZeroRows = 16;  // rows looked over by one of the trailing workgr
 
 // Workgroup p < pairs: pair p.  The pairs of a token follow one another on
 // one XCD, so its gradient row comes from HBM once and from that XCD's L2
-// for the other choices (4096 x 8 x 7168 to E4M3: 158 us with streaming loads
-// of it, 144 us, 5.4 TB/s, without).  The workgroups behind the pairs clear
-// the rows without a pair.
+// for the other choices (4096 x 8 x 7168 to E4M3: 160 us with the pairs dealt
+// to the XCDs in turn, 158 us with streaming loads of that row, 144 us, 5.4
+// TB/s, as it is; two to eight choices a workgroup, or the next chunk's loads
+// ahead, change nothing).  The workgroups behind the pairs clear the rows
+// without a pair.
 template <bool DF32, bool YF32, bool POW2, bool VEC>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   __shared__ float part[4];

@@ -19,8 +19,12 @@
 //   - the tiles of a gradient row by row instead of column by column: 446 us
 //     (writes alone, every group empty: 332 us against 385);
 //   - groups interleaved (tile rows of all groups in turn, or panels of 2 to
-//     16 rows), a persistent grid with the next tile's loads under the last
-//     block of this one: 452-482 us and 453-517 us, not kept.
+//     16 rows, or the fullest group with the emptiest), a persistent grid with
+//     the next tile's loads under the last block of this one, both blocks of a
+//     short loop loaded at once: no faster (452-482, 451-459, 453-517, 433
+//     against 433 us), not kept.
+// What bounds it now: the writes take 332 us alone and the products 326 us
+// alone; together the power and the memory they share give 433-454.
 #include "fp8q_internal.h"
 #include "quant_common.h"
 
@@ -62,6 +66,7 @@ struct WgArgs {
   bool vec_c;
   int rows, n, k;
   int tiles_m, tiles_n;
+  int region_m, region_n, xcds_n;  // tiles of an XCD's region, XCDs along n
 };
 
 // 16-byte chunk swizzle of a 128-byte LDS row (16 rows reading one logical
@@ -123,15 +128,18 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
   constexpr int TM = S::kTM, TN = S::kTN, E = TM + TN, WM = TM / 64;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
 
-  // Grid = groups x tiles of one gradient, row by row: the workgroups that
-  // run together write neighbouring 512-byte (1 KiB) pieces of the same rows.
-  // Workgroup i runs on XCD i % 8, so with a multiple of eight tiles a row an
-  // XCD keeps to its own columns and their X codes stay in its L2.
-  const int per = g.tiles_m * g.tiles_n;
+  // Grid = groups x 8 XCDs x the tiles of an XCD's region of a gradient (row
+  // by row, so that the workgroups that run together write neighbouring
+  // pieces of the same rows); workgroup i runs on XCD i % 8.
+  const int per = 8 * g.region_m * g.region_n;
   const int gi = blockIdx.x / per;
   const int in = blockIdx.x - gi * per;
-  const int tm = in / g.tiles_n;
-  const int m0 = tm * TM, n0 = (in - tm * g.tiles_n) * TN;
+  const int xcd = in & 7, idx = in >> 3;
+  const int rm = idx / g.region_n;
+  const int tm = xcd / g.xcds_n * g.region_m + rm;
+  const int tn = xcd % g.xcds_n * g.region_n + idx - rm * g.region_n;
+  if (tm >= g.tiles_m || tn >= g.tiles_n) return;  // (regions past the edge)
+  const int m0 = tm * TM, n0 = tn * TN;
   const int mrows = min(TM, g.rows - m0), nrows = min(TN, g.n - n0);
   // offsets outside [0, k], decreasing or off the 128-token blocks are
   // clamped and rounded down: every access stays inside the operands
@@ -355,7 +363,23 @@ template <class S, int JN>
 void launch(WgArgs g, int groups, int acc, hipStream_t stream) {
   g.tiles_m = (g.rows + S::kTM - 1) / S::kTM;
   g.tiles_n = (g.n + S::kTN - 1) / S::kTN;
-  const dim3 grid(g.tiles_m * g.tiles_n * groups), block(S::kThreads);
+  // Each XCD reads the codes of its region's rows and columns through its own
+  // L2: of the ways to lay eight regions over the tiles, the one with the
+  // smallest border.  (7168 x 2048, 16 groups: 8192 rows 319 -> 282 us and
+  // 32768 rows 846 -> 816 us against eight regions side by side, 256 x 256
+  // tiles, power-of-two float32 form; nothing to gain or lose within 2% where
+  // the writes decide.)
+  int best = 0;
+  for (int xn = 1; xn <= 8; xn *= 2) {
+    const int xm = 8 / xn, rm = (g.tiles_m + xm - 1) / xm, rn = (g.tiles_n + xn - 1) / xn;
+    if (!best || rm + rn < best) {
+      best = rm + rn;
+      g.region_m = rm;
+      g.region_n = rn;
+      g.xcds_n = xn;
+    }
+  }
+  const dim3 grid(8 * g.region_m * g.region_n * groups), block(S::kThreads);
   switch (acc) {
     case 1: hipLaunchKernelGGL((wgrad_grouped_kernel<S, JN, 1>), grid, block, 0, stream, g); break;
     case 2: hipLaunchKernelGGL((wgrad_grouped_kernel<S, JN, 2>), grid, block, 0, stream, g); break;
@@ -376,6 +400,16 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
 #ifdef FORCE
   const bool large = FORCE == 1;
 #else
+  // Forms that accumulate in the matrix core need half the vector work per
+  // product on 256 x 256 tiles (a W fragment is widened for 64 rows either
+  // way, an A fragment for 128 columns instead of 64).  That pays once a tile
+  // has enough blocks to hide that a compute unit holds one such tile and not
+  // two, and there are tiles for all units: 4096 x 7168, 16 groups,
+  // power-of-two float32 form, 2.5 / 4.6 / 8.7 blocks a group: 421 / 578 / 883
+  // us against 403 / 602 / 946 on 128 x 128; 7168 x 2048, 16.6 blocks: 824
+  // against 910 (hardware scales: 606 against 718).  The folded form is VALU-
+  // bound on either (1112 against 1062 us at 8.7 blocks) and spills on the
+  // large one.
   const int64_t tiles = (int64_t)((nout + Large::kTM - 1) / Large::kTM) * ((kin + Large::kTN - 1) / Large::kTN) * groups;
   const bool large = cap / BK >= 4 * groups && tiles >= device_cus();
 #endif

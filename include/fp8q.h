@@ -442,8 +442,8 @@ fp8q_status fp8q_swiglu_backward(const void* x, const float* x_scales, int64_t r
  * them down to 128, so a broken table gives wrong gradients but no access
  * outside the operands.  An empty group writes zeros.  dw float32
  * [G, Nout, ld_dw >= Kin], overwritten.  Partials at float32 grade.  Each
- * code operand is below 2 GiB, and G * ceil(Nout/128) * ceil(Kin/128) <
- * 2^24, else FP8Q_ERR_SHAPE. */
+ * code operand is below 2 GiB, and G * (ceil(Nout/128) + 7) *
+ * (ceil(Kin/128) + 7) < 2^24, else FP8Q_ERR_SHAPE. */
 fp8q_status fp8q_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales,
                                const uint8_t* x_t, const float* x_scales,
                                const int32_t* offsets, int32_t G, int64_t rows_cap,
