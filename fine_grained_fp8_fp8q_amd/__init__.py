@@ -636,8 +636,8 @@ def moe_combine_backward(dout, y, row_of, weights=None, token=None, bf16=True, q
     if (dt, dn) != (tokens, n):
         raise ValueError(f"dout must be [{tokens}, {n}], got [{dt}, {dn}]")
     if token is not None:
-        _need(token, torch.int32, "token")
-        if token.dim() != 1 or token.numel() != cap or not token.is_contiguous():
+        if token.dtype != torch.int32 or token.shape != (cap,) or not token.is_contiguous():
+            _need(token, torch.int32, "token")
             raise ValueError(f"token must be a contiguous int32 tensor of {cap} rows")
     dev = _one_device(y, dout, row_of, weights, token)
     dy = y.new_empty((cap, n), dtype=torch.bfloat16) if bf16 else None

@@ -83,8 +83,8 @@ fp8q_status fp8q_moe_combine_backward(const void* dout, int dout_dtype, int64_t 
   if ((pairs > 0 && ld_dout < N) || (dweights && rows_cap > 0 && ld_y < N) || (rows_out && dy_bf16 && ld_dy < N) ||
       (rows_out && dy_codes && ld_codes < N))
     return FP8Q_ERR_SHAPE;
-  // one workgroup per pair, and one per 16 rows to look for rows without one
-  if (pairs + rows_cap / 16 + 1 >= kMaxGroups) return FP8Q_ERR_SHAPE;
+  // one workgroup per pair, and one per four rows to look for rows without one
+  if (pairs + rows_cap / 4 + 1 >= kMaxGroups) return FP8Q_ERR_SHAPE;
   if (!aligned16(dout) || !aligned16(y) || !aligned16(row_of) || !aligned16(weights) || !aligned16(token) ||
       !aligned16(dy_bf16) || !aligned16(dy_codes) || !aligned16(dy_scales) || !aligned16(dweights))
     return FP8Q_ERR_ALIGN;
