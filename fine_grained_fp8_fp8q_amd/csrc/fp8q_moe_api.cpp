@@ -11,6 +11,8 @@ using namespace fp8q::checks;
 namespace {
 bool dtype_ok(int d) { return d == FP8Q_OUT_F32 || d == FP8Q_OUT_BF16; }
 bool mode_ok(int m) { return m == FP8Q_SCALE_FREE || m == FP8Q_SCALE_POW2; }
+// columns of a row that a workgroup goes over in steps (the step past the end fits in 32 bits)
+constexpr int64_t kMaxRow = int64_t(1) << 30;
 }  // namespace
 
 extern "C" {
@@ -57,7 +59,7 @@ fp8q_status fp8q_moe_combine(const void* y, int y_dtype, int64_t rows_cap, int64
   if (!out || (topk > 0 && !row_of) || (rows_cap > 0 && !y)) return FP8Q_ERR_INVALID_ARG;
   if (ld_out < N || (rows_cap > 0 && ld_y < N)) return FP8Q_ERR_SHAPE;
   // one workgroup per token and at least 512 columns
-  if (topk > kMaxDim / tokens || (N + 511) / 512 * tokens >= kMaxGroups) return FP8Q_ERR_SHAPE;
+  if (N >= kMaxRow || topk > kMaxDim / tokens || (N + 511) / 512 * tokens >= kMaxGroups) return FP8Q_ERR_SHAPE;
   if (!aligned16(out) || !aligned16(row_of) || !aligned16(weights) || !aligned16(y)) return FP8Q_ERR_ALIGN;
   if (fp8q_status st = check_device()) return st;
   return launched(fp8q::launch_moe_combine(y, y_dtype == FP8Q_OUT_F32, (int)rows_cap, (int)N, ld_y, row_of, weights,
@@ -84,7 +86,7 @@ fp8q_status fp8q_moe_combine_backward(const void* dout, int dout_dtype, int64_t 
       (rows_out && dy_codes && ld_codes < N))
     return FP8Q_ERR_SHAPE;
   // one workgroup per pair, and one per four rows to look for rows without one
-  if (pairs + rows_cap / 4 + 1 >= kMaxGroups) return FP8Q_ERR_SHAPE;
+  if (N >= kMaxRow || pairs + rows_cap / 4 + 1 >= kMaxGroups) return FP8Q_ERR_SHAPE;
   if (!aligned16(dout) || !aligned16(y) || !aligned16(row_of) || !aligned16(weights) || !aligned16(token) ||
       !aligned16(dy_bf16) || !aligned16(dy_codes) || !aligned16(dy_scales) || !aligned16(dweights))
     return FP8Q_ERR_ALIGN;

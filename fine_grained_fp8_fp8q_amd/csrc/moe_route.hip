@@ -424,9 +424,9 @@ hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t
   // Rows that a GEMM has just written are in the 256 MB Infinity Cache as
   // long as all of them fit beside the output: plain loads find them there
   // (87 MB of rows for 8192 tokens: 27 us against 34 with streaming loads,
-  // float32 out 38 against 52).  More rows are streamed (448 MB: 88 us against 95;
-  // 112 MB: 23 against 25).
-  const bool keep = (int64_t)cap * ldy * (y_f32 ? 4 : 2) <= (int64_t)96 << 20;
+  // float32 out 38 against 52).  More rows are streamed (448 MB: 88 us
+  // against 95; 112 MB: 23 against 25).
+  const bool keep = cap <= ((int64_t)96 << 20) / (ldy * (y_f32 ? 4 : 2));
   with_flag(n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0, [&](auto vec) {
     with_flag(keep, [&](auto kept) {
       constexpr bool V = decltype(vec)::value, K = decltype(kept)::value;

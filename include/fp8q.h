@@ -376,7 +376,7 @@ fp8q_status fp8q_moe_sort(const void* experts, int index_dtype, int64_t tokens, 
  * [tokens, topk], or NULL for the plain sum, which is also the gradient of
  * fp8q_gather_rows' row copy: dX[t] = sum over the rows of t.  Non-finite
  * values of y follow float32 arithmetic; rows no pair names are not read.
- * tokens * ceil(N/512) < 2^24, else FP8Q_ERR_SHAPE. */
+ * N < 2^30 and tokens * ceil(N/512) < 2^24, else FP8Q_ERR_SHAPE. */
 fp8q_status fp8q_moe_combine(const void* y, int y_dtype, int64_t rows_cap, int64_t N, int64_t ld_y,
                              const int32_t* row_of, const float* weights, int64_t tokens, int64_t topk,
                              int out_dtype, void* out, int64_t ld_out, hipStream_t stream);
@@ -397,7 +397,7 @@ fp8q_status fp8q_moe_combine(const void* y, int y_dtype, int64_t rows_cap, int64
  * zero values, codes and scales; with token NULL rows that no pair names are
  * left as they were.  No two pairs may name the same row.  For the quantized
  * form every product must be a finite BF16 value.
- * tokens * topk + rows_cap/4 < 2^24 - 1, else FP8Q_ERR_SHAPE. */
+ * N < 2^30 and tokens * topk + rows_cap/4 < 2^24 - 1, else FP8Q_ERR_SHAPE. */
 fp8q_status fp8q_moe_combine_backward(const void* dout, int dout_dtype, int64_t tokens, int64_t N, int64_t ld_dout,
                                       const void* y, int y_dtype, int64_t rows_cap, int64_t ld_y,
                                       const int32_t* row_of, const float* weights, int64_t topk,

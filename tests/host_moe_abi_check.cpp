@@ -99,6 +99,9 @@ int main() {
   CHECK(fp8q_moe_combine(P, 0, 100, 8, 8, I, F, big, big, 0, P, 8, nullptr) == FP8Q_ERR_SHAPE);
   CHECK(fp8q_moe_combine(P, 0, 100, 512, 512, I, F, 1 << 24, 1, 0, P, 512, nullptr) == FP8Q_ERR_SHAPE);
   CHECK(fp8q_moe_combine(P, 0, 100, 512, 512, I, F, (1 << 24) - 1, 1, 0, P, 512, nullptr) == FP8Q_OK);
+  CHECK(fp8q_moe_combine(P, 0, 1, 1 << 30, 1 << 30, I, F, 1, 1, 0, P, 1 << 30, nullptr) == FP8Q_ERR_SHAPE);
+  CHECK(fp8q_moe_combine(P, 0, 1, (1 << 30) - 1, 1 << 30, I, F, 1, 1, 0, P, 1 << 30, nullptr) == FP8Q_OK);
+  CHECK(fp8q_moe_combine_backward(P, 0, 1, 1 << 30, 1 << 30, P, 0, 1, 1 << 30, I, F, 1, I, P, 1 << 30, 0, nullptr, 0, nullptr, F, nullptr) == FP8Q_ERR_SHAPE);
   CHECK(fp8q_moe_combine(nullptr, 0, 0, 64, 0, I, nullptr, 10, 4, 0, P, 64, nullptr) == FP8Q_OK);  // no rows: zeros
 
   // backward: y is handed over only for the weight gradient
