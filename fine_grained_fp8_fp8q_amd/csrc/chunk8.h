@@ -94,7 +94,7 @@ __device__ __forceinline__ Raw<F32, W> ld_raw(const void* base, int64_t at, int 
   if (left >= W) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at * (F32 ? 2 : 1);
     if constexpr (Raw<F32, W>::N == 2) {
-      const uint2 c = KEEP ? *reinterpret_cast<const uint2*>(p) : ld_codes8(reinterpret_cast<const uint8_t*>(p), 8, aligned);
+      const uint2 c = KEEP && aligned ? *reinterpret_cast<const uint2*>(p) : ld_codes8(reinterpret_cast<const uint8_t*>(p), 8, aligned);
       r.w[0] = c.x;
       r.w[1] = c.y;
     } else {

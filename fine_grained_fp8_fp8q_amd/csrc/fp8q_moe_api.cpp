@@ -134,6 +134,8 @@ fp8q_status fp8q_grouped_wgrad_ex(const uint8_t* dy_t, const float* dy_scales, c
   // one workgroup of 256 threads per 128 x 128 outputs, and eight regions of
   // whole tiles: at most seven rows and columns of them more
   const int64_t tiles = ((Nout + 127) / 128 + 7) * ((Kin + 127) / 128 + 7);
+  // (the offsets of a tile's 256 rows, past the operand's last included, fit in 32 bits)
+  if (rows_cap >= int64_t(1) << 24) return FP8Q_ERR_SHAPE;
   if (Nout * rows_cap >= kMaxOperandBytes || Kin * rows_cap >= kMaxOperandBytes || tiles >= kMaxGroups ||
       tiles * G >= kMaxGroups)
     return FP8Q_ERR_SHAPE;

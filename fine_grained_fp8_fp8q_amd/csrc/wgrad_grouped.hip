@@ -155,7 +155,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
 
   // ---- loads.  One wave instruction moves 8 rows x 128 B of codes into LDS;
   // rows past the operand's last read as zero (the buffer's range check,
-  // which counts dwords).
+  // which counts dwords; 256 rows of fewer than 2^24 tokens stay below 2^32).
   const uint32_t rowb = (uint32_t)g.k, kofs0 = (uint32_t)kb0 * BK;
   const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(g.a + (size_t)m0 * rowb + kofs0), 0, (int)((uint32_t)mrows * rowb - kofs0), kRsrcFlags);
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
   };
 
   v4f acc[4][JN];
-    #pragma unroll
+#pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
     for (int j = 0; j < JN; ++j) acc[f][j] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -235,9 +235,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
         alo[f] = a_lo(f);
         ahi[f] = a_hi(f);
       }
-      v4i w0lo = w_lo(0), w0hi = w_hi(0), wlo, whi;
-        wlo = w_lo(1);
-      whi = w_hi(1);
+      v4i w0lo = w_lo(0), w0hi = w_hi(0), wlo = w_lo(1), whi = w_hi(1);
       v4f p[4], swj = v4f{0.f, 0.f, 0.f, 0.f};
       auto fold = [&](int j, int f) {
 #pragma unroll

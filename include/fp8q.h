@@ -441,8 +441,8 @@ fp8q_status fp8q_swiglu_backward(const void* x, const float* x_scales, int64_t r
  * the kernel does not report: it clamps offsets to [0, rows_cap] and rounds
  * them down to 128, so a broken table gives wrong gradients but no access
  * outside the operands.  An empty group writes zeros.  dw float32
- * [G, Nout, ld_dw >= Kin], overwritten.  Partials at float32 grade.  Each
- * code operand is below 2 GiB, and G * (ceil(Nout/128) + 7) *
+ * [G, Nout, ld_dw >= Kin], overwritten.  Partials at float32 grade.
+ * rows_cap < 2^24, each code operand is below 2 GiB, and G * (ceil(Nout/128) + 7) *
  * (ceil(Kin/128) + 7) < 2^24, else FP8Q_ERR_SHAPE. */
 fp8q_status fp8q_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales,
                                const uint8_t* x_t, const float* x_scales,

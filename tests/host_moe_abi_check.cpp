@@ -122,6 +122,8 @@ int main() {
   CHECK(fp8q_grouped_wgrad_ex(U, F, U, F, I, 3, 256, 20, 30, 3, F, 30, nullptr) == FP8Q_OK && g_name == "wgrad" && g_a == 3 && g_b == 256 && g_c == 200030 && g_d == 3);
   CHECK(fp8q_grouped_wgrad(U, F, U, F, I, std::numeric_limits<int32_t>::max(), 256, 20, 30, F, 30, nullptr) == FP8Q_ERR_SHAPE);
   CHECK(fp8q_grouped_wgrad(U, F, U, F, I, 2, big - 127, big, big, F, big, nullptr) == FP8Q_ERR_SHAPE);
+  CHECK(fp8q_grouped_wgrad(U, F, U, F, I, 2, 1 << 24, 20, 30, F, 30, nullptr) == FP8Q_ERR_SHAPE);
+  CHECK(fp8q_grouped_wgrad(U, F, U, F, I, 2, (1 << 24) - 128, 20, 30, F, 30, nullptr) == FP8Q_OK);
   CHECK(fp8q_grouped_wgrad(U, F, U, F, I, 2, 0, 20, 30, F, 30, nullptr) == FP8Q_OK);  // no rows: zeros
 
   g_result = hipErrorInvalidValue;
