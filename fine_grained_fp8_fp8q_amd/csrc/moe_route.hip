@@ -301,7 +301,7 @@ __device__ __forceinline__ void clear_row(uint8_t* p, int64_t bytes) {
 // TB/s, as it is; two to eight choices a workgroup, or the next chunk's loads
 // ahead, change nothing).  The workgroups behind the pairs clear the rows
 // without a pair.
-template <bool DF32, bool YF32, bool POW2, bool VEC>
+template <bool DF32, bool YF32, bool POW2, bool VEC, bool KEEP>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
   __shared__ float part[4];
   const int tid = threadIdx.x;
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
     if (in) {
       const auto gr = ld_raw<DF32, 8, true>(a.dout, (int64_t)t * a.lddo + col, left, VEC);
       Raw<YF32, 8> v = {};
-      if (a.y) v = ld_raw<YF32, 8>(a.y, (int64_t)row * a.ldy + col, left, VEC);
+      if (a.y) v = ld_raw<YF32, 8, KEEP>(a.y, (int64_t)row * a.ldy + col, left, VEC);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         g[i] = gr.at(i);
@@ -421,12 +421,7 @@ hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t
   const int items = (n + 7) / 8, threads = row_threads(n);
   const int chunks = (items + threads - 1) / threads;
   const dim3 grid((unsigned)(tokens * chunks)), block(threads);
-  // Rows that a GEMM has just written are in the 256 MB Infinity Cache as
-  // long as all of them fit beside the output: plain loads find them there
-  // (87 MB of rows for 8192 tokens: 27 us against 34 with streaming loads,
-  // float32 out 38 against 52).  More rows are streamed (448 MB: 88 us
-  // against 95; 112 MB: 23 against 25).
-  const bool keep = cap <= ((int64_t)96 << 20) / (ldy * (y_f32 ? 4 : 2));
+  const bool keep = input_stays_cached(cap, ldy * (y_f32 ? 4 : 2));
   with_flag(n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0, [&](auto vec) {
     with_flag(keep, [&](auto kept) {
       constexpr bool V = decltype(vec)::value, K = decltype(kept)::value;
@@ -451,12 +446,14 @@ hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int toke
   const int zero = token && (dy || codes) ? (cap + kZeroRows - 1) / kZeroRows : 0;
   const dim3 grid(a.pairs + zero), block(row_threads(n));
   with_flag(whole, [&](auto vec) {
-    constexpr bool V = decltype(vec)::value;
-    auto kernel = dout_f32 ? (y_f32 ? (pow2 ? combine_bwd_kernel<true, true, true, V> : combine_bwd_kernel<true, true, false, V>)
-                                    : (pow2 ? combine_bwd_kernel<true, false, true, V> : combine_bwd_kernel<true, false, false, V>))
-                           : (y_f32 ? (pow2 ? combine_bwd_kernel<false, true, true, V> : combine_bwd_kernel<false, true, false, V>)
-                                    : (pow2 ? combine_bwd_kernel<false, false, true, V> : combine_bwd_kernel<false, false, false, V>));
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
+    with_flag(y && input_stays_cached(cap, ldy * (y_f32 ? 4 : 2)), [&](auto kept) {
+      with_flag(pow2, [&](auto p2) {
+        constexpr bool V = decltype(vec)::value, K = decltype(kept)::value, P = decltype(p2)::value;
+        auto kernel = dout_f32 ? (y_f32 ? combine_bwd_kernel<true, true, P, V, K> : combine_bwd_kernel<true, false, P, V, K>)
+                               : (y_f32 ? combine_bwd_kernel<false, true, P, V, K> : combine_bwd_kernel<false, false, P, V, K>);
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
+      });
+    });
   });
   return hipGetLastError();
 }

@@ -67,7 +67,7 @@ __device__ __forceinline__ void widen8(uint4 c, float scale, float* v) {
 // another.  One pass, four tiles a wave: 32768 x 2048 from the cache with y
 // takes 107 us (6.3 TB/s); a grid of 2048 workgroups that loop with the next
 // tiles' loads in flight takes 124.
-template <bool CACHE, bool QUANT, bool POW2, bool VEC>
+template <bool CACHE, bool QUANT, bool POW2, bool VEC, bool KEEP>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
   const int lane = threadIdx.x & 63;
   const int sub = lane & 15;
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
   float sg = 1.0f, su = 1.0f;
   if constexpr (CACHE) {
     const uint8_t* src = static_cast<const uint8_t*>(a.x) + (int64_t)row * a.ldx + col;
-    const uint2 gc = ld_codes8(src, left, VEC), uc = ld_codes8(src + a.inter, left, VEC);
+    const uint2 gc = ld_codes8<KEEP>(src, left, VEC), uc = ld_codes8<KEEP>(src + a.inter, left, VEC);
     cg = make_uint4(gc.x, gc.y, 0, 0);
     cu = make_uint4(uc.x, uc.y, 0, 0);
     if (left > 0) {
@@ -93,10 +93,10 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
     }
   } else {
     const uint16_t* src = static_cast<const uint16_t*>(a.x) + (int64_t)row * a.ldx + col;
-    cg = ld_bf16x8(src, left, VEC);
-    cu = ld_bf16x8(src + a.inter, left, VEC);
+    cg = ld_bf16x8<KEEP>(src, left, VEC);
+    cu = ld_bf16x8<KEEP>(src + a.inter, left, VEC);
   }
-  const uint4 cd = ld_bf16x8(a.dy + (int64_t)row * a.lddy + col, left, VEC);
+  const uint4 cd = ld_bf16x8<KEEP>(a.dy + (int64_t)row * a.lddy + col, left, VEC);
 
   float g[8], u[8], d[8], dg[8], du[8], y[8];
   widen8<CACHE>(cg, sg, g);
@@ -135,12 +135,23 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
   }
 }
 
-template <bool CACHE, bool VEC>
+template <bool CACHE, bool VEC, bool KEEP>
 void launch(const SwigluBwdArgs& a, bool pow2, hipStream_t stream) {
   const int grid = (int)(((int64_t)a.ntiles + 15) / 16);  // < 2^24
-  auto kernel = !a.codes ? swiglu_bwd_kernel<CACHE, false, false, VEC>
-                         : pow2 ? swiglu_bwd_kernel<CACHE, true, true, VEC> : swiglu_bwd_kernel<CACHE, true, false, VEC>;
+  auto kernel = !a.codes ? swiglu_bwd_kernel<CACHE, false, false, VEC, KEEP>
+                : pow2   ? swiglu_bwd_kernel<CACHE, true, true, VEC, KEEP>
+                         : swiglu_bwd_kernel<CACHE, true, false, VEC, KEEP>;
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, a);
+}
+
+// VEC: whole 8-element chunks on 16-byte (codes: 8-byte) boundaries
+template <bool CACHE>
+void launch_form(const SwigluBwdArgs& a, bool vec, bool keep, bool pow2, hipStream_t stream) {
+  if (vec) {
+    keep ? launch<CACHE, true, true>(a, pow2, stream) : launch<CACHE, true, false>(a, pow2, stream);
+  } else {  // (unaligned loads are plain ones)
+    launch<CACHE, false, true>(a, pow2, stream);
+  }
 }
 
 }  // namespace
@@ -153,13 +164,13 @@ hipError_t launch_swiglu_backward(const void* x, const float* xscales, int rows,
   a.x = x; a.xscales = xscales; a.ldx = ldx; a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
   a.codes = codes; a.ldc = ldc; a.scales = scales; a.y = y; a.ldy = ldy;
   a.inter = inter; a.nb = (inter + 127) / 128; a.ntiles = rows * a.nb;  // < 2^28 (checked by the entry point)
-  // VEC: whole 8-element chunks on 16-byte (codes: 8-byte) boundaries
   const bool vec = inter % 8 == 0 && ldx % 8 == 0 && lddy % 8 == 0 && (!dx || lddx % 8 == 0) &&
                    (!codes || ldc % 8 == 0) && (!y || ldy % 8 == 0);
+  const bool keep = input_stays_cached(rows, (xscales ? 1 : 2) * ldx + 2 * lddy);
   if (xscales) {
-    vec ? launch<true, true>(a, pow2, stream) : launch<true, false>(a, pow2, stream);
+    launch_form<true>(a, vec, keep, pow2, stream);
   } else {
-    vec ? launch<false, true>(a, pow2, stream) : launch<false, false>(a, pow2, stream);
+    launch_form<false>(a, vec, keep, pow2, stream);
   }
   return hipGetLastError();
 }
