@@ -476,19 +476,25 @@ def swiglu_quantize(x, scale_mode="free", cache=False, cache_scale_mode="pow2"):
 
 def _one_device(first, *others):
     """The device of the tensors given (None among them is skipped)."""
-    dev = first.device
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
+    return first.device
+
+
+_stream_handle = None
 
 
 def _raw_stream(dev):
     """Handle of the current stream of dev; asked for without making a
     torch.cuda.Stream of it (1.8 us) where torch has the call for that."""
-    torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(dev.index) if get else torch.cuda.current_stream(dev).cuda_stream
+    global _stream_handle
+    if _stream_handle is None:
+        torch = _torch()
+        _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _stream_handle(dev.index)
 
 
 def _call(dev, name, *args):
@@ -506,8 +512,20 @@ def _call(dev, name, *args):
 
 
 def _addr(t):
-    """Address of a tensor's data, None (NULL) for none and for an empty one."""
-    return t.data_ptr() if t is not None and t.numel() else None
+    """Address of a tensor's data, None (NULL) for none; 0 (NULL) for an empty one."""
+    return None if t is None else t.data_ptr()
+
+
+def _new(rows, cols, dtype, dev):
+    """A new dense [rows, cols] tensor (0.3 us less than torch.empty)."""
+    return _torch().empty_strided((rows, cols), (cols or 1, 1), dtype=dtype, device=dev)
+
+
+def _new_codes(rows, cols, dev):
+    """A new uint8 [rows, cols] tensor whose row stride is a multiple of 16, and that stride."""
+    torch = _torch()
+    ld = _pad16(max(cols, 1))
+    return torch.empty_strided((rows, cols), (ld, 1), dtype=torch.uint8, device=dev), ld
 
 
 def _rows_of(t, name, dtypes):
@@ -544,14 +562,15 @@ def _types():
 
 def _pair_table(row_of, weights):
     """Checks row_of and weights: contiguous [tokens, topk]."""
-    if row_of.dtype != _types()[2] or not row_of.is_cuda or row_of.dim() != 2 or not row_of.is_contiguous():
+    shape = row_of.shape
+    if row_of.dtype != _types()[2] or len(shape) != 2 or not row_of.is_contiguous():
         _need(row_of, _types()[2], "row_of")
         raise ValueError("row_of must be a contiguous int32 [tokens, topk] tensor")
-    if weights is not None and (weights.dtype != _types()[1][0] or weights.shape != row_of.shape or
+    if weights is not None and (weights.dtype != _types()[1][0] or weights.shape != shape or
                                 not weights.is_contiguous()):
         _contig_f32(weights, "weights")
         raise ValueError("weights must have the shape of row_of")
-    return row_of.shape
+    return shape
 
 
 def moe_sort(experts, num_hosted, first=0, align=1, rows_cap=None):
@@ -587,8 +606,8 @@ def moe_sort(experts, num_hosted, first=0, align=1, rows_cap=None):
     _call(experts.device, "fp8q_moe_sort", experts_p, INDEX_I64 if experts.dtype == torch.int64 else INDEX_I32, tokens,
           topk, ld, first, num_hosted, align, rows_cap, p, p + 4 * n0, p + 4 * (n0 + n1),
           p + 4 * (n0 + n1 + n2) if need else None, need)
-    return (buf[:num_hosted + 1], buf[n0:n0 + rows_cap],
-            buf.as_strided((tokens, topk), (topk, 1), buf.storage_offset() + n0 + n1))
+    return (buf.as_strided((num_hosted + 1,), (1,)), buf.as_strided((rows_cap,), (1,), n0),
+            buf.as_strided((tokens, topk), (topk or 1, 1), n0 + n1))
 
 
 def moe_combine(y, row_of, weights=None, out_dtype=None, out=None):
@@ -607,7 +626,7 @@ def moe_combine(y, row_of, weights=None, out_dtype=None, out=None):
         out_dtype = out_dtype or types[OUT_BF16]
         if out_dtype not in types:
             raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-        out, ldo = y.new_empty((tokens, n), dtype=out_dtype), max(n, 1)
+        out, ldo = _new(tokens, n, out_dtype, dev), max(n, 1)
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out has another type than out_dtype")
@@ -640,15 +659,14 @@ def moe_combine_backward(dout, y, row_of, weights=None, token=None, bf16=True, q
             _need(token, torch.int32, "token")
             raise ValueError(f"token must be a contiguous int32 tensor of {cap} rows")
     dev = _one_device(y, dout, row_of, weights, token)
-    dy = y.new_empty((cap, n), dtype=torch.bfloat16) if bf16 else None
+    dy = _new(cap, n, torch.bfloat16, dev) if bf16 else None
     codes = scales = dw = None
     ldc = n
     if quantize:
-        codes = _alloc_codes(cap, n, dev)
-        ldc = codes.stride(0)
-        scales = y.new_empty((cap, (n + 127) // 128), dtype=torch.float32)
+        codes, ldc = _new_codes(cap, n, dev)
+        scales = _new(cap, (n + 127) // 128, torch.float32, dev)
     if want_dweights:
-        dw = y.new_empty((tokens, topk), dtype=torch.float32)
+        dw = _new(tokens, topk, torch.float32, dev)
     _call(dev, "fp8q_moe_combine_backward", dout_p, types.index(dout.dtype), tokens, n, ldd, y_p, types.index(y.dtype), cap,
           ldy, _addr(row_of), _addr(weights), topk, _addr(token), _addr(dy), max(n, 1), _scale_mode(scale_mode), _addr(codes), ldc,
           _addr(scales), _addr(dw))
@@ -678,14 +696,13 @@ def swiglu_backward(x, dy, x_scales=None, bf16=True, quantize=False, scale_mode=
     if not (bf16 or quantize or want_y):
         raise ValueError("nothing to compute: ask for bf16, quantize or want_y")
     dev = _one_device(x, dy, x_scales)
-    dx = dy.new_empty((rows, two_inter)) if bf16 else None
-    y = dy.new_empty((rows, inter)) if want_y else None
+    dx = _new(rows, two_inter, torch.bfloat16, dev) if bf16 else None
+    y = _new(rows, inter, torch.bfloat16, dev) if want_y else None
     codes = scales = None
     ldc = two_inter
     if quantize:
-        codes = _alloc_codes(rows, two_inter, dev)
-        ldc = codes.stride(0)
-        scales = dy.new_empty((rows, two_inter // 128), dtype=torch.float32)
+        codes, ldc = _new_codes(rows, two_inter, dev)
+        scales = _new(rows, two_inter // 128, torch.float32, dev)
     _call(dev, "fp8q_swiglu_backward", x_p, _addr(x_scales), rows, inter, ldx, dy_p, lddy, _addr(dx), max(two_inter, 1),
           _scale_mode(scale_mode), _addr(codes), ldc, _addr(scales), _addr(y), max(inter, 1))
     return dx, y, codes, scales
