@@ -79,21 +79,15 @@ hipError_t launch_swiglu_quant(const uint16_t* x, int rows, int inter, int64_t l
                                float* cscales, hipStream_t stream);
 
 // Routing table (moe_route.hip): one workgroup alone up to kSortAlonePairs
-// pairs; above, workgroups of 1024, 2048 or 4096 pairs -- the fewest whose
-// count table (hist: int32 [blocks, groups], from a launch of its own, read
-// whole by each of them) stays below kSortTable entries -- and at most
-// kMaxSortBlocks of them.
+// pairs; above, as many workgroups of 1024 pairs or more as there are, at
+// most kMaxSortBlocks, after a launch that counts each one's pairs per expert
+// (hist: int32 [blocks, groups]).
 constexpr int kMaxSortGroups = 512;
 constexpr int kSortAlonePairs = 4096;
-constexpr int kSortTable = 8192;
 constexpr int kMaxSortBlocks = 256;
-inline int sort_blocks(int pairs, int groups) {
+inline int sort_blocks(int pairs) {
   if (pairs <= kSortAlonePairs) return 1;
-  int64_t blocks = 0;
-  for (int chunk = 1024; chunk <= 4096; chunk *= 2) {
-    blocks = ((int64_t)pairs + chunk - 1) / chunk;
-    if (blocks <= kMaxSortBlocks && blocks * groups <= kSortTable) break;
-  }
+  const int64_t blocks = ((int64_t)pairs + 1023) / 1024;
   return (int)(blocks < kMaxSortBlocks ? blocks : kMaxSortBlocks);
 }
 hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, int64_t ld, int64_t first, int groups,

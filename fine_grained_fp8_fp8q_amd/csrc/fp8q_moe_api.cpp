@@ -20,7 +20,7 @@ extern "C" {
 int64_t fp8q_moe_sort_workspace(int64_t tokens, int64_t topk, int32_t G) {
   if (!dim_ok(tokens) || !dim_ok(topk) || G <= 0 || tokens == 0 || topk == 0) return 0;
   if (topk > kMaxDim / tokens) return 0;
-  const int blocks = fp8q::sort_blocks((int)(tokens * topk), G);
+  const int blocks = fp8q::sort_blocks((int)(tokens * topk));
   return blocks > 1 ? (int64_t)blocks * G * (int64_t)sizeof(int32_t) : 0;
 }
 

@@ -20,12 +20,16 @@ namespace fp8q {
 namespace {
 
 // ------------------------------------------------------------------ sort ---
-// Bound by latency: 16384 x 8 pairs are 1.6 MB in and out, and the two
-// launches take 3.1 and 6.1 us (a single workgroup, for a few thousand pairs
-// or fewer, 4.5 us).  A count per workgroup costs the second launch a read of
-// the whole table, which is cheaper than one workgroup that goes over all
-// pairs twice from about 4096 pairs on, and unlike one pass with a running
-// total handed on it has nobody wait for another workgroup.
+// Bound by latency: 16384 x 8 pairs over 16 of 256 experts are 1.6 MB in and
+// out, and the two launches take 7.5 us together (replayed from a graph; over
+// all 256 experts 10.0 us, 800,000 pairs 17.7 us; one token's pairs, one
+// launch, 4.0 us).  The second launch reads the whole table of counts in
+// every workgroup, column by column into registers (one LDS atomic per entry
+// instead: 18.5 us at 256 experts); unlike one pass with a running total
+// handed on, nobody waits for another workgroup.  The first pass of a chunk
+// counts with plain LDS atomics, only the second needs the order within a
+// wave (ranks by ballots in both: 10.0 instead of 8.2 us for 4096 pairs in one
+// workgroup).
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
 struct SortArgs {
@@ -68,16 +72,14 @@ __device__ __forceinline__ int index_bits(int groups) { return groups > 1 ? 32 -
 template <typename IDX>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   __shared__ int cnt[kMaxSortGroups];
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
   for (int e = tid; e < a.groups; e += kSortThreads) cnt[e] = 0;
   __syncthreads();
-  const int bits = index_bits(a.groups);
   const int64_t p0 = (int64_t)blockIdx.x * a.chunk;
   for (int i = 0; i < a.chunk; i += kSortThreads) {
     const int64_t p = p0 + i + tid;
     const int e = p < a.pairs ? local_expert<IDX>(a, (int)p) : -1;
-    const uint64_t same = same_expert(e, bits);
-    if (same && lane == __builtin_ctzll(same)) atomicAdd(&cnt[e], __builtin_popcountll(same));
+    if (e >= 0) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
   for (int e = tid; e < a.groups; e += kSortThreads) a.hist[(int64_t)blockIdx.x * a.groups + e] = cnt[e];
@@ -115,8 +117,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   __syncthreads();
 
   auto count = [&](int e) {
-    const uint64_t same = same_expert(e, bits);
-    if (same && lane == __builtin_ctzll(same)) atomicAdd(&cnt[wave * G + e], __builtin_popcountll(same));
+    if (e >= 0) atomicAdd(&cnt[wave * G + e], 1);
   };
 #pragma unroll
   for (int s = 0; s < kHeld; ++s)
@@ -125,13 +126,18 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   // pairs of each expert in all chunks, and in the chunks before this one
   // (kept in start[] until the group starts are known)
   if (blocks > 1) {
-    for (int i = tid; i < blocks * G; i += kSortThreads) {
-      const int b = i / G, e = i - b * G;
-      const int h = a.hist[i];
-      if (h) {
-        atomicAdd(&total[e], h);
-        if (b < blk) atomicAdd(&start[e], h);
+    const int stride = 1 << bits;  // threads e, e + stride, ... add up the column of expert e
+    const int e = tid & (stride - 1), parts = kSortThreads >> bits;
+    if (e < G) {
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int b = tid >> bits; b < blocks; b += parts) {
+        const int h = a.hist[b * G + e];
+        all += h;
+        before += b < blk ? h : 0;
       }
+      if (all) atomicAdd(&total[e], all);
+      if (before) atomicAdd(&start[e], before);
     }
   }
   __syncthreads();
@@ -385,7 +391,7 @@ hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, i
   SortArgs a{};
   a.experts = experts; a.topk = topk; a.ld = ld; a.first = first; a.groups = groups; a.align = align;
   a.pairs = pairs; a.cap = cap; a.offsets = offsets; a.token = token; a.row_of = row_of; a.hist = hist;
-  const int blocks = sort_blocks(pairs, groups);
+  const int blocks = sort_blocks(pairs);
   const int64_t per = ((int64_t)pairs + blocks - 1) / blocks;
   a.chunk = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
   if (a.chunk == 0) a.chunk = kSortThreads;
