@@ -395,9 +395,6 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
   WgArgs g{};
   g.a = dy_t; g.sa = dy_scales; g.w = x_t; g.sw = x_scales; g.offsets = offsets; g.c = dw; g.ldc = lddw;
   g.vec_c = lddw % 4 == 0; g.rows = nout; g.n = kin; g.k = cap;
-#ifdef FORCE
-  const bool large = FORCE == 1;
-#else
   // Forms that accumulate in the matrix core need half the vector work per
   // product on 256 x 256 tiles (a W fragment is widened for 64 rows either
   // way, an A fragment for 128 columns instead of 64).  That pays once a tile
@@ -410,7 +407,6 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
   // large one.
   const int64_t tiles = (int64_t)((nout + Large::kTM - 1) / Large::kTM) * ((kin + Large::kTN - 1) / Large::kTN) * groups;
   const bool large = cap / BK >= 4 * groups && tiles >= device_cus();
-#endif
   if (acc == 0 || !large) {
     launch<Small, 4>(g, groups, acc, stream);
   } else {
