@@ -17,16 +17,6 @@ struct __attribute__((packed, aligned(1))) Any8 {
   uint32_t w[2];
 };
 
-// Streaming (non-temporal) loads pass the 256 MB Infinity Cache by.  An input
-// that the kernel before has just written is found there by plain loads as
-// long as all of it fits beside the output; a larger one is streamed.
-// Measured, plain against streaming loads, inputs in rotation: combine of 87
-// MB of rows 27 against 34 us (float32 out 38 against 52), 112 MB 25 against
-// 23, 448 MB 95 against 88; combine backward of 59 MB 17.6 against 21.2, 117
-// MB 41 against 39; SwiGLU backward from 34 MB of cache and gradient 13.6
-// against 16.4, 67 MB 25.6 against 29.4, 134 MB 58 against 57.
-inline bool input_stays_cached(int64_t rows, int64_t row_bytes) { return rows <= ((int64_t)96 << 20) / row_bytes; }
-
 // Eight BF16 values; those past `left` (which may be <= 0) are +0.  KEEP: a
 // plain load instead of a streaming one.
 template <bool KEEP = false>

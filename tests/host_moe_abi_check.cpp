@@ -103,6 +103,9 @@ int main() {
   CHECK(fp8q_moe_combine(P, 0, 1, (1 << 30) - 1, 1 << 30, I, F, 1, 1, 0, P, 1 << 30, nullptr) == FP8Q_OK);
   CHECK(fp8q_moe_combine_backward(P, 0, 1, 1 << 30, 1 << 30, P, 0, 1, 1 << 30, I, F, 1, I, P, 1 << 30, 0, nullptr, 0, nullptr, F, nullptr) == FP8Q_ERR_SHAPE);
   CHECK(fp8q_moe_combine(nullptr, 0, 0, 64, 0, I, nullptr, 10, 4, 0, P, 64, nullptr) == FP8Q_OK);  // no rows: zeros
+  // ... and the rule that the launch asks takes an input of no bytes
+  CHECK(fp8q::input_stays_cached(0, 0) && fp8q::input_stays_cached(big, 0) && fp8q::input_stays_cached(0, 4 * big));
+  CHECK(fp8q::input_stays_cached(96, 1 << 20) && !fp8q::input_stays_cached(97, 1 << 20) && !fp8q::input_stays_cached(big, 4 * big));
 
   // backward: y is handed over only for the weight gradient
   CHECK(fp8q_moe_combine_backward(P, 1, 10, 64, 64, P, 1, 100, 64, I, F, 4, I, P, 64, 1, U, 64, F, F, nullptr) == FP8Q_OK);

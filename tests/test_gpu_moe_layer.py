@@ -188,6 +188,19 @@ def test_combine_empty():
     assert fp8q.moe_combine(y, rows[:0]).shape == (0, 16)
 
 
+def test_no_rows_and_no_row_stride():
+    """rows_cap = 0 with ld_y = 0: the sum and its gradient with respect to the weights are zero."""
+    lib = fp8q.load_library()
+    rows = torch.zeros((5, 2), dtype=torch.int32, device="cuda:0")
+    dout = torch.ones((5, 16), dtype=torch.bfloat16, device="cuda:0")
+    out, dw = torch.full((5, 16), 7.0, device="cuda:0"), torch.full((5, 2), 7.0, device="cuda:0")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.fp8q_moe_combine(None, 1, 0, 16, 0, rows.data_ptr(), None, 5, 2, 0, out.data_ptr(), 16, stream) == fp8q.OK
+    assert lib.fp8q_moe_combine_backward(dout.data_ptr(), 1, 5, 16, 16, out.data_ptr(), 1, 0, 0, rows.data_ptr(), None, 2, None,
+                                         None, 0, 0, None, 0, None, dw.data_ptr(), stream) == fp8q.OK
+    assert (host(out) == 0).all() and (host(dw) == 0).all()
+
+
 # ------------------------------------------------------ combine backward ----
 
 @pytest.mark.parametrize("ddt", [torch.bfloat16, torch.float32])
