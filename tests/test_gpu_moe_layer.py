@@ -408,7 +408,8 @@ def test_refusals_of_the_binding():
                 lambda: fp8q.moe_combine(y, rows, out=y), lambda: fp8q.moe_combine_backward(y, y, rows),
                 lambda: fp8q.moe_combine_backward(y[:4], y, rows, None, rows[:, 0].contiguous()),
                 lambda: fp8q.swiglu_backward(y, y), lambda: fp8q.swiglu_backward(y, y[:, :8], quantize=True),
-                lambda: fp8q.swiglu_backward(y, y[:, :8], bf16=False)):
+                lambda: fp8q.swiglu_backward(y, y[:, :8], bf16=False), lambda: fp8q.moe_sort(rows, -1), lambda: fp8q.moe_sort(rows, 4, align=0),
+                lambda: fp8q.moe_sort(rows, 4, align=(1 << 32) + 1, rows_cap=0), lambda: fp8q.moe_sort(rows, (1 << 32) + 1, rows_cap=8)):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(fp8q.Fp8qError):  # rows over one another
