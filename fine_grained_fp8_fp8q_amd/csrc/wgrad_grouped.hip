@@ -41,19 +41,23 @@ typedef __attribute__((address_space(3))) void* lds_void_ptr;
 constexpr int BK = 128;
 constexpr int kRsrcFlags = 0x00020000;
 
-// WM x WN waves of 64 x 16 JN outputs.  A stage holds one K block: TM rows of
-// dY^T, then TN of X^T, 128 B each.  Threads, rows of a stage and scale
-// entries are equal in number: thread e owns the scales of stage row e.
-template <int WM, int WN, int JN>
+// WM x WN waves of 16 FM x 16 JN outputs.  A stage holds one K block: TM rows
+// of dY^T, then TN of X^T, 128 B each.
+template <int WM, int WN, int FM, int JN>
 struct Shape {
-  static constexpr int kTM = 64 * WM, kTN = 16 * JN * WN, kThreads = 64 * WM * WN;
-  static constexpr int kStage = (kTM + kTN) * BK;
-  static constexpr int kScaleHalf = 4 * (kTM + kTN) * 4;  // scales of four K blocks, [block][entry]
+  static constexpr int kWM = WM, kFM = FM, kJN = JN, kTM = 16 * FM * WM, kTN = 16 * JN * WN;
+  static constexpr int kThreads = 64 * WM * WN, kE = kTM + kTN;  // scale entries: one per stage row
+  static constexpr int kStage = kE * BK;
+  static constexpr int kScaleHalf = 4 * kE * 4;  // scales of four K blocks, [block][entry]
   static constexpr int kLds = 2 * kStage + 2 * kScaleHalf;
-  static_assert(kTM == kTN && kTM + kTN == kThreads, "one thread per stage row");
+  static constexpr int kLoads = kTM / (8 * WM * WN);  // load instructions of a wave per K block and operand
+  static constexpr int kScales = 4 * kE / kThreads;   // scales of four K blocks that a thread brings
+  static_assert(kTM == kTN && kTM % 64 == 0 && kLoads * 8 * WM * WN == kTM && kLoads <= 4 && kScales * kThreads == 4 * kE,
+                "whole waves for each operand");
 };
-using Large = Shape<4, 2, 8>;  // 256 x 256: one workgroup per compute unit
-using Small = Shape<2, 2, 4>;  // 128 x 128: two
+using Large = Shape<4, 2, 4, 8>;   // 256 x 256: one workgroup per compute unit
+using Medium = Shape<2, 2, 4, 4>;  // 128 x 128: two
+using Small = Shape<2, 2, 2, 2>;   // 64 x 64: four
 
 struct WgArgs {
   const uint8_t* a;   // dY^T codes [rows, k]
@@ -123,9 +127,9 @@ __device__ __forceinline__ void k_loop(int nkb, uint8_t* __restrict__ s0, uint8_
 
 // ACC as FP8Q_ACC_*: 0 float32 grade, 1 FP8 matrix core, 2 hardware scales,
 // 3 float32 grade with power-of-two scales.
-template <class S, int JN, int ACC>
+template <class S, int ACC>
 __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g) {
-  constexpr int TM = S::kTM, TN = S::kTN, E = TM + TN, WM = TM / 64;
+  constexpr int TM = S::kTM, TN = S::kTN, E = S::kE, WM = S::kWM, FM = S::kFM, JN = S::kJN, LI = S::kLoads, SB = S::kScales;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
 
   // Grid = groups x 8 XCDs x the tiles of an XCD's region of a gradient (row
@@ -150,7 +154,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & (WM - 1), wn = wave / WM;
   const int r16 = lane & 15, c0 = 2 * (lane >> 4);
-  const int arow0 = wm * 64 + r16, wrow0 = wn * 16 * JN + r16;
+  const int arow0 = wm * 16 * FM + r16, wrow0 = wn * 16 * JN + r16;
   const int asw = swz(arow0), wsw = swz(wrow0);  // the same for rows + 16 f
 
   // ---- loads.  One wave instruction moves 8 rows x 128 B of codes into LDS;
@@ -163,47 +167,48 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
       (void*)(g.w + (size_t)n0 * rowb + kofs0), 0, (int)((uint32_t)nrows * rowb - kofs0), kRsrcFlags);
   uint32_t r_off[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = (wave * 4 + i) * 8 + (lane >> 3);
+  for (int i = 0; i < LI; ++i) {
+    const int row = (wave * LI + i) * 8 + (lane >> 3);
     r_off[i] = (uint32_t)row * rowb + 16u * (uint32_t)((lane & 7) ^ swz(row));
   }
   auto issue = [&](int kb, uint8_t* st) {
     const uint32_t kofs = (uint32_t)kb * BK;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (lds_void_ptr)(st + (wave * 4 + i) * 1024), 16, r_off[i], kofs, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rsrc, (lds_void_ptr)(st + TM * BK + (wave * 4 + i) * 1024), 16, r_off[i], kofs, 0, 0);
+    for (int i = 0; i < LI; ++i) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (lds_void_ptr)(st + (wave * LI + i) * 1024), 16, r_off[i], kofs, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rsrc, (lds_void_ptr)(st + TM * BK + (wave * LI + i) * 1024), 16, r_off[i], kofs, 0, 0);
     }
   };
-  // Scales: the four blocks of a group come with one load per thread (past
-  // the group's or the row's end they are other blocks' scales, which no
-  // product uses, or zero) a whole group ahead, and go to LDS
+  // Scales: of the four blocks of a group a thread brings SB for one stage
+  // row (past the group's or the row's end they are other blocks' scales,
+  // which no product uses, or zero) a whole group ahead, and puts them in LDS
   // [block][entry], into the half the group uses.
   const uint32_t sblk = (uint32_t)(g.k / BK) * 4u, sofs0 = (uint32_t)kb0 * 4u;
-  const bool a_side = wave < TM / 64;
+  const int ent = tid & (E - 1), sb0 = wave * 64 / E * SB;  // stage row, first of the thread's blocks
+  const bool a_side = (wave * 64 & (E - 1)) < TM;           // (the same for a whole wave)
   const float* sp = a_side ? g.sa + (size_t)m0 * (sblk >> 2) : g.sw + (size_t)n0 * (sblk >> 2);
   const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(sp + kb0), 0, (int)((uint32_t)(a_side ? mrows : nrows) * sblk - sofs0), kRsrcFlags);
-  const uint32_t s_off = (uint32_t)(a_side ? tid : tid - TM) * sblk;
-  float sreg[4];
+  const uint32_t s_off = (uint32_t)(a_side ? ent : ent - TM) * sblk + 4u * (uint32_t)sb0;
+  float sreg[SB];
   auto fetch_scales = [&](int grp) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < SB; ++b)
       sreg[b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(s_rsrc, s_off + 16u * (uint32_t)grp + 4u * b, 0, 0));
   };
   auto put_scales = [&](int grp, uint8_t* scl) {
     float* half = reinterpret_cast<float*>(scl + (grp & 1) * S::kScaleHalf);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) half[b * E + tid] = sreg[b];
+    for (int b = 0; b < SB; ++b) half[(sb0 + b) * E + ent] = sreg[b];
   };
 
-  v4f acc[4][JN];
+  v4f acc[FM][JN];
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
+  for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int j = 0; j < JN; ++j) acc[f][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  // ---- one K block of a wave: JN W fragments x 4 A fragments.  The MFMA
+  // ---- one K block of a wave: JN W fragments x FM A fragments.  The MFMA
   // computes the transposed tile, so a lane owns output row m = r16 of a
   // fragment and four consecutive columns.
   auto compute = [&](const uint8_t* st, const float* Sc) {
@@ -215,9 +220,9 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
     auto w_hi = [&](int j) { return *reinterpret_cast<const v4i*>(Wb + j * 2048 + 16 * ((c0 + 1) ^ wsw)); };
     const float* Sw = Sc + TM + wn * 16 * JN;
     if constexpr (ACC == 0 || ACC == 3) {
-      float sa[4], sw[ACC == 3 ? JN : 1];
+      float sa[FM], sw[ACC == 3 ? JN : 1];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) sa[f] = Sc[arow0 + f * 16];
+      for (int f = 0; f < FM; ++f) sa[f] = Sc[arow0 + f * 16];
       if constexpr (ACC == 3) {
 #pragma unroll
         for (int j = 0; j < JN; ++j) sw[j] = Sw[j * 16 + r16];
@@ -228,15 +233,15 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
       };
       auto sa_of = [&](int f) { return ACC == 3 ? sa[f] : 1.0f; };
       auto sw_of = [&](int j) { return ACC == 3 ? sw[ACC == 3 ? j : 0] : 1.0f; };
-      v8bf af[4][4], bf[4];
-      v4i alo[4], ahi[4];
+      v8bf af[FM][4], bf[4];
+      v4i alo[FM], ahi[FM];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
+      for (int f = 0; f < FM; ++f) {
         alo[f] = a_lo(f);
         ahi[f] = a_hi(f);
       }
       v4i w0lo = w_lo(0), w0hi = w_hi(0), wlo = w_lo(1), whi = w_hi(1);
-      v4f p[4], swj = v4f{0.f, 0.f, 0.f, 0.f};
+      v4f p[FM], swj = v4f{0.f, 0.f, 0.f, 0.f};
       auto fold = [&](int j, int f) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[f][j][v] = __builtin_fmaf(p[f][v], sa[f] * swj[v], acc[f][j][v]);
@@ -248,11 +253,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
           if (j == 0) {
             bf[q] = part(w0lo, w0hi, q, sw_of(0));
 #pragma unroll
-            for (int f = 0; f < 4; ++f) af[f][q] = part(alo[f], ahi[f], q, sa_of(f));
+            for (int f = 0; f < FM; ++f) af[f][q] = part(alo[f], ahi[f], q, sa_of(f));
             __builtin_amdgcn_sched_barrier(0);
           }
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
+          for (int f = 0; f < FM; ++f) {
             if constexpr (ACC == 3) {
               acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[q], af[f][q], acc[f][j], 0, 0, 0);
             } else {
@@ -272,17 +277,17 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
       }
       if constexpr (ACC == 0) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f) fold(JN - 1, f);
+        for (int f = 0; f < FM; ++f) fold(JN - 1, f);
       }
     } else {
       auto cat = [](v4i lo, v4i hi) { return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}; };
       auto e8m0 = [](float x) { return (int)((__float_as_uint(x) >> 23) & 0xFFu); };
-      v8i af[4], wf[2];
-      float sa[4];
-      int ae[4], we[JN];
+      v8i af[FM], wf[2];
+      float sa[FM];
+      int ae[FM], we[JN];
       wf[0] = cat(w_lo(0), w_hi(0));
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
+      for (int f = 0; f < FM; ++f) {
         af[f] = cat(a_lo(f), a_hi(f));
         sa[f] = Sc[arow0 + f * 16];
         ae[f] = e8m0(sa[f]);
@@ -294,16 +299,16 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
         if (j < JN - 1) wf[(j + 1) & 1] = cat(w_lo(j + 1), w_hi(j + 1));
         if constexpr (ACC == 2) {
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
+          for (int f = 0; f < FM; ++f)
             acc[f][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[j & 1], af[f], acc[f][j], 0, 0, 0, we[j], 0, ae[f]);
         } else {
           const v4f swj = *reinterpret_cast<const v4f*>(Sw + j * 16 + 4 * (lane >> 4));
-          v4f p[4];
+          v4f p[FM];
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
+          for (int f = 0; f < FM; ++f)
             p[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[j & 1], af[f], v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
+          for (int f = 0; f < FM; ++f)
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[f][j][v] = __builtin_fmaf(p[f][v], sa[f] * swj[v], acc[f][j][v]);
         }
@@ -312,7 +317,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
     }
   };
 
-  const int mw = mrows - wm * 64, nw = nrows - wn * 16 * JN;  // rows and columns of the wave that exist
+  const int mw = mrows - wm * 16 * FM, nw = nrows - wn * 16 * JN;  // rows and columns of the wave that exist
   if (nkb > 0) {
     auto comp = [&](const uint8_t* st, const uint8_t* scl, int kb) {
       if (mw > 0 && nw > 0) compute(st, reinterpret_cast<const float*>(scl + ((kb >> 2) & 1) * S::kScaleHalf) + (kb & 3) * E);
@@ -328,19 +333,19 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
   if (mw <= 0 || nw <= 0) return;
   constexpr int CH = 4 * JN, RI = 64 / CH;  // 16-byte chunks of a row, rows of a store instruction
   uint8_t* tile = lds + wave * 16 * CH * 16;
-  const uint32_t put = (uint32_t)r16 * (16 * CH), putx = 16u * (uint32_t)((lane >> 4) ^ r16);
+  const uint32_t put = (uint32_t)r16 * (16 * CH), putx = 16u * (uint32_t)((lane >> 4) ^ (r16 & (CH - 1)));
   const int lr = lane / CH, ch = lane & (CH - 1);
   const uint64_t voff = ((uint64_t)lr * (uint64_t)g.ldc + 4u * (uint32_t)ch) * 4u;
-  uint8_t* cw = reinterpret_cast<uint8_t*>(g.c + ((int64_t)gi * g.rows + m0 + wm * 64) * g.ldc + n0 + wn * 16 * JN);
-  const bool full = g.vec_c && mw >= 64 && nw >= 16 * JN;
+  uint8_t* cw = reinterpret_cast<uint8_t*>(g.c + ((int64_t)gi * g.rows + m0 + wm * 16 * FM) * g.ldc + n0 + wn * 16 * JN);
+  const bool full = g.vec_c && mw >= 16 * FM && nw >= 16 * JN;
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
+  for (int f = 0; f < FM; ++f) {
 #pragma unroll
     for (int j = 0; j < JN; ++j) *reinterpret_cast<v4f*>(tile + put + (putx ^ (uint32_t)(64 * j))) = acc[f][j];
 #pragma unroll
     for (int i = 0; i < JN; ++i) {
       const int row = i * RI + lr;
-      const v4f v = *reinterpret_cast<const v4f*>(tile + row * (16 * CH) + 16 * (ch ^ row));
+      const v4f v = *reinterpret_cast<const v4f*>(tile + row * (16 * CH) + 16 * (ch ^ (row & (CH - 1))));
       float* dst = reinterpret_cast<float*>(cw + (int64_t)(f * 16 + i * RI) * g.ldc * 4 + voff);
       if (full) {
         __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(dst));
@@ -357,7 +362,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
   }
 }
 
-template <class S, int JN>
+template <class S>
 void launch(WgArgs g, int groups, int acc, hipStream_t stream) {
   g.tiles_m = (g.rows + S::kTM - 1) / S::kTM;
   g.tiles_n = (g.n + S::kTN - 1) / S::kTN;
@@ -379,11 +384,11 @@ void launch(WgArgs g, int groups, int acc, hipStream_t stream) {
   }
   const dim3 grid(8 * g.region_m * g.region_n * groups), block(S::kThreads);
   switch (acc) {
-    case 1: hipLaunchKernelGGL((wgrad_grouped_kernel<S, JN, 1>), grid, block, 0, stream, g); break;
-    case 2: hipLaunchKernelGGL((wgrad_grouped_kernel<S, JN, 2>), grid, block, 0, stream, g); break;
-    case 3: hipLaunchKernelGGL((wgrad_grouped_kernel<S, JN, 3>), grid, block, 0, stream, g); break;
+    case 1: hipLaunchKernelGGL((wgrad_grouped_kernel<S, 1>), grid, block, 0, stream, g); break;
+    case 2: hipLaunchKernelGGL((wgrad_grouped_kernel<S, 2>), grid, block, 0, stream, g); break;
+    case 3: hipLaunchKernelGGL((wgrad_grouped_kernel<S, 3>), grid, block, 0, stream, g); break;
     default:
-      if constexpr (JN == 4) hipLaunchKernelGGL((wgrad_grouped_kernel<S, JN, 0>), grid, block, 0, stream, g);
+      if constexpr (S::kJN <= 4) hipLaunchKernelGGL((wgrad_grouped_kernel<S, 0>), grid, block, 0, stream, g);
   }
 }
 
@@ -395,6 +400,17 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
   WgArgs g{};
   g.a = dy_t; g.sa = dy_scales; g.w = x_t; g.sw = x_scales; g.offsets = offsets; g.c = dw; g.ldc = lddw;
   g.vec_c = lddw % 4 == 0; g.rows = nout; g.n = kin; g.k = cap;
+  // Tiles of 64 x 64 where larger ones leave compute units without work: fewer
+  // tiles of 128 x 128 than three quarters of the units, or, as groups are
+  // uneven and the fullest is the last, fewer than half of them in a group and
+  // five for every two in all.  Groups x outputs, rows in all, float32 form,
+  // against 128 x 128: 1 x 512 x 512, 16384 rows 65 and 156 us; 4 x 512 x 512,
+  // 4096 rows 12.1 and 25.6; 8 x 1024 x 1024, 16384 rows 46 and 67; 16 x 768 x
+  // 768 (576 tiles), 16384 rows 39 and 56; past the rule 1 x 2048 x 2048, 16384
+  // rows 172 and 158, 16 x 1024 x 1024 (1024 tiles), 4096 rows 22.9 and 20.1.
+  // (Four K blocks in flight instead of two, or eight waves a tile: nothing
+  // gained.)
+  //
   // Forms that accumulate in the matrix core need half the vector work per
   // product on 256 x 256 tiles (a W fragment is widened for 64 rows either
   // way, an A fragment for 128 columns instead of 64).  That pays once a tile
@@ -402,15 +418,23 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
   // two, and there are tiles for all units: 4096 x 7168, 16 groups,
   // power-of-two float32 form, 2.5 / 4.6 / 8.7 blocks a group: 421 / 578 / 883
   // us against 403 / 602 / 946 on 128 x 128; 7168 x 2048, 16.6 blocks: 824
-  // against 910 (hardware scales: 606 against 718).  The folded form is VALU-
-  // bound on either (1112 against 1062 us at 8.7 blocks) and spills on the
-  // large one.
-  const int64_t tiles = (int64_t)((nout + Large::kTM - 1) / Large::kTM) * ((kin + Large::kTN - 1) / Large::kTN) * groups;
-  const bool large = cap / BK >= 4 * groups && tiles >= device_cus();
-  if (acc == 0 || !large) {
-    launch<Small, 4>(g, groups, acc, stream);
+  // against 910 (hardware scales: 606 against 718).  Groups are uneven: of
+  // several the fullest alone has to keep a quarter of the units busy, and all
+  // of them two tiles for each (16 x 1024 x 2048, 16384 rows: 111 against 77
+  // us; 4 x 2048 x 2048, 4096 rows: 53 against 43; 16 x 2048 x 2048, 8192 rows:
+  // 88 against 93; one group of 4096 x 4096, 4096 rows: 103 against 121).  The
+  // folded form is VALU-bound on either (1112 against 1062 us at 8.7 blocks)
+  // and spills on the large one.
+  const auto tiles = [&](int t) { return (int64_t)((nout + t - 1) / t) * ((kin + t - 1) / t) * groups; };
+  const int cus = device_cus();
+  const bool fills = groups == 1 ? tiles(256) >= cus : tiles(256) >= 2 * cus && 4 * tiles(256) >= (int64_t)cus * groups;
+  const bool few = 4 * tiles(128) <= 3 * cus || (2 * tiles(128) <= 5 * cus && 2 * tiles(128) <= (int64_t)cus * groups);
+  if (few) {
+    launch<Small>(g, groups, acc, stream);
+  } else if (acc == 0 || cap / BK < 4 * groups || !fills) {
+    launch<Medium>(g, groups, acc, stream);
   } else {
-    launch<Large, 8>(g, groups, acc, stream);
+    launch<Large>(g, groups, acc, stream);
   }
   return hipGetLastError();
 }

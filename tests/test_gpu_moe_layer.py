@@ -343,7 +343,8 @@ def token_operand(r, width, cap, real, mode, std=1.0):
 @pytest.mark.parametrize("acc,mode", [("fp32", "free"), ("fp32", "pow2"), ("fp32_pow2", "pow2"), ("fp8_mfma", "free"), ("fp8_mfma_scaled", "pow2")])
 @pytest.mark.parametrize("nout,kin,sizes", [(1, 1, [5]), (40, 72, [0, 130, 0, 1]), (256, 256, [128, 256, 384]), (300, 260, [700, 0, 65]),
                                             (257, 225, [0, 0]), (512, 448, [1, 128, 129, 1000]), (3, 600, [640] * 9),
-                                            (2000, 4100, [700, 400])])  # (enough 256 x 256 tiles, and tokens, for the large shape)
+                                            (2000, 4100, [700, 400]),  # (on 128 x 128 tiles, the smaller ones before on 64 x 64)
+                                            (2000, 8200, [900, 700]), (4000, 4100, [600])])  # (enough 256 x 256 tiles, and tokens, for the large shape)
 def test_grouped_wgrad(acc, mode, nout, kin, sizes):
     r = np.random.default_rng(nout)
     padded = [-(-s // 128) * 128 for s in sizes]
