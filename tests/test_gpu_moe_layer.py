@@ -115,10 +115,10 @@ def check_sort_by_rules(experts, first, groups, align, cap):
 
 @pytest.mark.parametrize("tokens,topk,experts,first,groups,align", [
     (150001, 8, 64, 0, 64, 128), (400003, 3, 9, 2, 5, 1), (262145, 4, 512, 0, 512, 16), (1100000, 1, 3, 0, 3, 1), (2048, 2, 4, 0, 4, 1),
-    (2049, 2, 4, 0, 4, 1)])
+    (2049, 2, 4, 0, 4, 1), (2000, 1, 8, 0, 8, 2048), (9000, 2, 5, 1, 3, 1500), (40, 2, 160, 0, 160, 1024)])
 def test_sort_of_many_pairs(tokens, topk, experts, first, groups, align):
-    """More pairs than the kernel keeps in registers between its passes (above a million), and both sides of the
-    size from which more than one workgroup counts."""
+    """More pairs than the kernel keeps in registers between its passes (above a million), both sides of the
+    size from which more than one workgroup counts, and long paddings."""
     e = np.random.default_rng(tokens).integers(0, experts, size=(tokens, topk))
     cap = -(-(tokens * topk + groups * align) // align) * align
     check_sort_by_rules(e, first, groups, align, cap)
