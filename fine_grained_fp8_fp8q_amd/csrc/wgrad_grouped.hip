@@ -25,6 +25,8 @@
 //     against 433 us), not kept.
 // What bounds it now: the writes take 332 us alone and the products 326 us
 // alone; together the power and the memory they share give 433-454.
+#include <type_traits>
+
 #include "fp8q_internal.h"
 #include "quant_common.h"
 
@@ -34,6 +36,7 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef v4f v4f_any __attribute__((aligned(4)));  // on any element's boundary
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_void_ptr;
@@ -67,7 +70,6 @@ struct WgArgs {
   const int32_t* offsets;
   float* c;
   int64_t ldc;
-  bool vec_c;
   int rows, n, k;
   int tiles_m, tiles_n;
   int region_m, region_n, xcds_n;  // tiles of an XCD's region, XCDs along n
@@ -327,8 +329,12 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
 
   // ---- epilogue: 16 rows (one M fragment) at a time through the wave's own
   // part of the stages, so that a store instruction writes whole rows of
-  // 64 JN bytes.  Non-temporal: through the caches the outputs push the
-  // operands, which other tiles still read, out of the L2.
+  // 64 JN bytes.  Rows on 64-byte boundaries go out non-temporal: through the
+  // caches the outputs push the operands, which other tiles still read, out
+  // of the L2 (16 x 2290 x 3184, 4096 rows: 129 us, cached 157).  Rows off
+  // them start and end inside a line, which the L2 puts together (16 x 2290 x
+  // 3189: 176 us, non-temporal 181, element by element 255; 45 rows: 130, 174
+  // and 213).
   __syncthreads();
   if (mw <= 0 || nw <= 0) return;
   constexpr int CH = 4 * JN, RI = 64 / CH;  // 16-byte chunks of a row, rows of a store instruction
@@ -337,28 +343,45 @@ __global__ __launch_bounds__(S::kThreads, 2) void wgrad_grouped_kernel(WgArgs g)
   const int lr = lane / CH, ch = lane & (CH - 1);
   const uint64_t voff = ((uint64_t)lr * (uint64_t)g.ldc + 4u * (uint32_t)ch) * 4u;
   uint8_t* cw = reinterpret_cast<uint8_t*>(g.c + ((int64_t)gi * g.rows + m0 + wm * 16 * FM) * g.ldc + n0 + wn * 16 * JN);
-  const bool full = g.vec_c && mw >= 16 * FM && nw >= 16 * JN;
-#pragma unroll
-  for (int f = 0; f < FM; ++f) {
-#pragma unroll
-    for (int j = 0; j < JN; ++j) *reinterpret_cast<v4f*>(tile + put + (putx ^ (uint32_t)(64 * j))) = acc[f][j];
-#pragma unroll
-    for (int i = 0; i < JN; ++i) {
-      const int row = i * RI + lr;
-      const v4f v = *reinterpret_cast<const v4f*>(tile + row * (16 * CH) + 16 * (ch ^ (row & (CH - 1))));
-      float* dst = reinterpret_cast<float*>(cw + (int64_t)(f * 16 + i * RI) * g.ldc * 4 + voff);
-      if (full) {
+  const bool full = mw >= 16 * FM && nw >= 16 * JN;
+  auto write = [&](auto streaming) {
+    auto store = [](float* dst, v4f v) {
+      if constexpr (decltype(streaming)::value) {
         __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(dst));
-      } else if (f * 16 + row < mw) {
-        if (g.vec_c && 4 * ch + 3 < nw) {
-          __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(dst));
-        } else {
+      } else {
+        *reinterpret_cast<v4f_any*>(dst) = v;
+      }
+    };
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (4 * ch + u < nw) dst[u] = v[u];
+    for (int f = 0; f < FM; ++f) {
+#pragma unroll
+      for (int j = 0; j < JN; ++j) *reinterpret_cast<v4f*>(tile + put + (putx ^ (uint32_t)(64 * j))) = acc[f][j];
+#pragma unroll
+      for (int i = 0; i < JN; ++i) {
+        const int row = i * RI + lr;
+        const v4f v = *reinterpret_cast<const v4f*>(tile + row * (16 * CH) + 16 * (ch ^ (row & (CH - 1))));
+        float* dst = reinterpret_cast<float*>(cw + (int64_t)(f * 16 + i * RI) * g.ldc * 4 + voff);
+        if (full) {
+          store(dst, v);
+        } else if (f * 16 + row < mw) {
+          if (4 * ch + 3 < nw) {
+            store(dst, v);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (4 * ch + u < nw) dst[u] = v[u];
+          }
         }
       }
     }
+  };
+  // (the scheduling barriers keep the compiler from making one store of the two kinds)
+  if (g.ldc % 16 == 0) {
+    write(std::true_type{});
+  } else {
+    __builtin_amdgcn_sched_barrier(0);
+    write(std::false_type{});
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -399,7 +422,7 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
                                 int kin, int acc, float* dw, int64_t lddw, hipStream_t stream) {
   WgArgs g{};
   g.a = dy_t; g.sa = dy_scales; g.w = x_t; g.sw = x_scales; g.offsets = offsets; g.c = dw; g.ldc = lddw;
-  g.vec_c = lddw % 4 == 0; g.rows = nout; g.n = kin; g.k = cap;
+  g.rows = nout; g.n = kin; g.k = cap;
   // Tiles of 64 x 64 where larger ones leave compute units without work: fewer
   // tiles of 128 x 128 than three quarters of the units, or, as groups are
   // uneven and the fullest is the last, fewer than half of them in a group and
