@@ -104,6 +104,28 @@ inline bool input_stays_cached(int64_t rows, int64_t row_bytes) {
   return row_bytes == 0 || rows <= ((int64_t)96 << 20) / row_bytes;
 }
 
+// Threads of a workgroup that goes over a row of n columns, eight a thread:
+// of 64, 128, 192 and 256 the one that leaves the fewest idle, the largest of
+// equals (7168 columns: 7 x 128; 1030: 192).
+inline int row_threads(int n) {
+  const int items = (n + 7) / 8;
+  int threads = 256;
+  for (int c = 192; c >= 64; c -= 64)
+    if ((items + c - 1) / c * c < (items + threads - 1) / threads * threads) threads = c;
+  return threads;
+}
+// Combine backward.  Few pairs wait for the loads of one step after another:
+// as few steps as there are (8 pairs of 6259 columns: 4 steps of 256 threads
+// 5.4 us, 13 of 64 10.1).  Many hide each other's: as few idle threads (32768
+// pairs of 7168 columns: 7 x 128 144 us, 4 x 256 149).  Rows of no columns
+// still have a weight gradient to write, and so one wave.
+inline int combine_backward_threads(int pairs, int n) {
+  if (pairs > 2048) return row_threads(n);
+  if (n == 0) return 64;
+  const int items = (n + 7) / 8, steps = (items + 255) / 256;
+  return ((items + steps - 1) / steps + 63) / 64 * 64;
+}
+
 hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t ldy, const int* row_of,
                               const float* weights, int tokens, int topk, bool out_f32, void* out, int64_t ldo,
                               hipStream_t stream);

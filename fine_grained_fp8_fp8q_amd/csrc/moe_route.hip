@@ -401,17 +401,6 @@ hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, i
   return i64 ? launch_sort<int64_t>(a, blocks, stream) : launch_sort<int32_t>(a, blocks, stream);
 }
 
-// Threads of a workgroup that goes over a row of n columns, eight a thread:
-// of 64, 128, 192 and 256 the one that leaves the fewest idle, the largest of
-// equals (7168 columns: 7 x 128; 1030: 192).
-static int row_threads(int n) {
-  const int items = (n + 7) / 8;
-  int threads = 256;
-  for (int c = 192; c >= 64; c -= 64)
-    if ((items + c - 1) / c * c < (items + threads - 1) / threads * threads) threads = c;
-  return threads;
-}
-
 // VEC: every row starts on a 16-byte boundary and has whole chunks, so the
 // kernels need no checks of a chunk's end (with them at every load the two
 // sums above take 97 and 74 us).
@@ -453,13 +442,7 @@ hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int toke
   a.pairs = tokens * topk; a.topk = topk; a.n = n; a.cap = cap;
   const bool whole = n % 8 == 0 && lddo % 8 == 0 && (!y || ldy % 8 == 0) && (!dy || lddy % 8 == 0) && (!codes || ldc % 8 == 0);
   const int zero = token && (dy || codes) ? (cap + kZeroRows - 1) / kZeroRows : 0;
-  // Few pairs wait for the loads of one step after another: as few steps as
-  // there are (8 pairs of 6259 columns: 4 steps of 256 threads 5.4 us, 13 of 64
-  // 10.1).  Many hide each other's: as few idle threads (32768 pairs of 7168
-  // columns: 7 x 128 144 us, 4 x 256 149).
-  const int items = (n + 7) / 8, steps = (items + 255) / 256;
-  const int threads = a.pairs <= 2048 ? ((items + steps - 1) / steps + 63) / 64 * 64 : row_threads(n);
-  const dim3 grid(a.pairs + zero), block(threads);
+  const dim3 grid(a.pairs + zero), block(combine_backward_threads(a.pairs, n));
   with_flag(whole, [&](auto vec) {
     with_flag(y && input_stays_cached(cap, ldy * (y_f32 ? 4 : 2)), [&](auto kept) {
       with_flag(pow2, [&](auto p2) {

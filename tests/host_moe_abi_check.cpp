@@ -119,6 +119,21 @@ int main() {
   CHECK(fp8q_moe_combine_backward(P, 0, big, 64, 64, P, 0, 100, 64, I, F, big, I, P, 64, 0, nullptr, 0, nullptr, F, nullptr) == FP8Q_ERR_SHAPE);
   CHECK(fp8q_moe_combine_backward(P, 0, 10, 64, 64, P, 0, big, 64, I, F, 4, I, P, 64, 0, nullptr, 0, nullptr, F, nullptr) == FP8Q_ERR_SHAPE);
 
+  // rows of no columns have weight gradients (zeros) all the same ...
+  g_calls = 0;
+  for (int64_t tokens : {int64_t(1), int64_t(10), int64_t(3000)})
+    CHECK(fp8q_moe_combine_backward(nullptr, 0, tokens, 0, 0, nullptr, 0, 100, 0, I, F, 4, I, nullptr, 0, 0, nullptr, 0, nullptr, F, nullptr) == FP8Q_OK &&
+          g_c == 0 && g_d == 4 * tokens);
+  CHECK(g_calls == 3);
+  // ... and every width that is accepted gets whole waves, no more than 256 threads, on both sides of the rule
+  for (int pairs : {1, 2048, 2049, 1 << 23})
+    for (int n : {0, 1, 8, 9, 511, 512, 513, 1030, 2047, 2048, 2049, 6259, 7168, (1 << 30) - 1}) {
+      const int threads = fp8q::combine_backward_threads(pairs, n);
+      CHECK(threads >= 64 && threads <= 256 && threads % 64 == 0);
+      if (pairs <= 2048 && n > 0) CHECK((int64_t)threads * 8 * ((n + 2047) / 2048) >= n);  // in the fewest steps
+    }
+  CHECK(fp8q::combine_backward_threads(8, 6259) == 256 && fp8q::combine_backward_threads(1 << 15, 7168) == 128);
+
   // swiglu, grouped wgrad
   CHECK(fp8q_swiglu_backward(P, F, 10, 128, 256, P, 128, P, 256, 1, U, 256, F, P, 128, nullptr) == FP8Q_OK && g_name == "swiglu" && g_c == 1);
   CHECK(fp8q_swiglu_backward(P, nullptr, big, big / 2, big, P, big, P, big, 0, nullptr, 0, nullptr, nullptr, 0, nullptr) == FP8Q_ERR_SHAPE);

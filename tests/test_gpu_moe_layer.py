@@ -268,6 +268,19 @@ def test_combine_backward_empty():
     assert not host(fp8q.moe_combine_backward(z(3, 40), z(0, 40), none)[3]).any()
 
 
+@pytest.mark.parametrize("tokens", [1, 3, 1024, 1025])
+def test_combine_backward_of_rows_without_columns(tokens):
+    """The weight gradients of an empty width are zeros, on both sides of 2048 pairs."""
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda:0")  # noqa: E731
+    rows = torch.arange(2 * tokens, dtype=torch.int32, device="cuda:0").view(tokens, 2) - 1
+    token = torch.full((2 * tokens,), -1, dtype=torch.int32, device="cuda:0")
+    for quantize in (False, True):
+        torch.full((tokens, 2), 7.0, device="cuda:0")  # (what the next allocation may find)
+        dy, codes, scales, dw = fp8q.moe_combine_backward(z(tokens, 0), z(2 * tokens, 0), rows, None, token, quantize=quantize)
+        assert dy.shape == (2 * tokens, 0) and dw.shape == (tokens, 2) and not host(dw).any()
+        assert codes is None if not quantize else codes.shape == (2 * tokens, 0) and scales.shape == (2 * tokens, 0)
+
+
 # ------------------------------------------------------- SwiGLU backward ----
 
 # (the FP8 cache has whole tiles)
