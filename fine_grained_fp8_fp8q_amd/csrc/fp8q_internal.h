@@ -90,6 +90,12 @@ inline int sort_blocks(int pairs) {
   const int64_t blocks = ((int64_t)pairs + 1023) / 1024;
   return (int)(blocks < kMaxSortBlocks ? blocks : kMaxSortBlocks);
 }
+// f(row) for the rows first + lane, first + lane + lanes, ... below end.  first
+// and end reach 2^31 - 1, so a row past the end is not a 32-bit number.
+template <class F>
+__host__ __device__ inline void for_rows(int first, int lane, int lanes, int end, F f) {
+  for (int64_t r = (int64_t)first + lane; r < end; r += lanes) f(r);
+}
 hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, int64_t ld, int64_t first, int groups,
                            int align, int cap, int* offsets, int* token, int* row_of, int* hist, hipStream_t stream);
 // Streaming (non-temporal) loads pass the 256 MB Infinity Cache by.  An input

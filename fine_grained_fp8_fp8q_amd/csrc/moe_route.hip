@@ -199,16 +199,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   // rows without a pair: the padding of every group (a group to a wave, 160
   // groups padded to 128 take 8.0 us instead of 23.2 with a group to the
   // workgroup; long paddings by all of it), and everything behind the last one
+  auto clear = [&](int64_t r) { a.token[r] = -1; };
   if (a.align > 1) {
     const bool all = a.align > kSortThreads;
     const int lanes = all ? kSortThreads : 64, first = all ? blk : blk * kSortWaves + wave;
-    for (int g = first; g < G; g += all ? blocks : blocks * kSortWaves) {
-      const int end = min(start[g + 1], a.cap);
-      for (int r = start[g] + total[g] + (all ? tid : lane); r < end; r += lanes) a.token[r] = -1;
-    }
+    for (int g = first; g < G; g += all ? blocks : blocks * kSortWaves)
+      for_rows(start[g] + total[g], all ? tid : lane, lanes, min(start[g + 1], a.cap), clear);
   }
-  for (int64_t r = (int64_t)start[G] + blk * kSortThreads + tid; r < a.cap; r += (int64_t)blocks * kSortThreads)
-    a.token[r] = -1;
+  for_rows(start[G], blk * kSortThreads + tid, blocks * kSortThreads, a.cap, clear);
 }
 
 // --------------------------------------------------------------- combine ---

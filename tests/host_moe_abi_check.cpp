@@ -89,6 +89,20 @@ int main() {
   CHECK(fp8q_moe_sort(P, 0, 16384, 8, 8, 0, 16, 1, 16, I, I, I, P, need - 1, nullptr) == FP8Q_ERR_INVALID_ARG);
   CHECK(fp8q_moe_sort(P, 0, 16384, 8, 8, 0, 16, 1, 16, I, I, I, nullptr, need, nullptr) == FP8Q_ERR_INVALID_ARG);
   CHECK(fp8q_moe_sort(P, 0, 16384, 8, 8, 0, 16, 1, 16, I, I, I, P, need, nullptr) == FP8Q_OK);
+  // the walk over padding rows ends at the largest rows that are accepted, for every lane and step of the kernel
+  CHECK(fp8q_moe_sort(P, 0, 1, 1, 1, 0, 1, (int32_t)big - 1, big - 1, I, I, I, nullptr, 0, nullptr) == FP8Q_OK);
+  CHECK(fp8q_moe_sort(P, 0, big - 2, 1, 1, 0, 1, 2, big - 1, I, I, I, P, 1 << 20, nullptr) == FP8Q_OK);
+  for (int first : {(int)big - 2, (int)big - 1100, (int)big - 1})
+    for (int lanes : {64, 1024, 256 * 1024}) {
+      int64_t seen = 0;
+      bool inside = true;
+      for (int lane = 0; lane < lanes; ++lane)
+        fp8q::for_rows(first, lane, lanes, (int)big - 1, [&](int64_t r) {
+          inside = inside && r >= first && r < big - 1;
+          ++seen;
+        });
+      CHECK(inside && seen == big - 1 - first);
+    }
   // no tokens: the table is still written
   CHECK(fp8q_moe_sort(nullptr, 0, 0, 8, 8, 0, 16, 1, 16, I, I, nullptr, nullptr, 0, nullptr) == FP8Q_OK && g_a == 0);
 
