@@ -587,8 +587,9 @@ def moe_sort(experts, num_hosted, first=0, align=1, rows_cap=None):
     """
     torch = _torch()
     tokens, topk, ld, experts_p = _rows_of(experts, "experts", (torch.int32, torch.int64))
-    if not 0 <= num_hosted < 1 << 31 or not 1 <= align < 1 << 31:  # (they go over as 32-bit integers)
-        raise ValueError("num_hosted must not be negative, align must be at least 1, both below 2^31")
+    # (num_hosted and align go over as 32-bit integers, first as a 64-bit one)
+    if not 0 <= num_hosted < 1 << 31 or not 0 <= first < 1 << 31 or not 1 <= align < 1 << 31:
+        raise ValueError("num_hosted and first must not be negative, align must be at least 1, all below 2^31")
     pairs = tokens * topk
     if rows_cap is None:
         rows_cap = (pairs + num_hosted * (align - 1) + align - 1) // align * align

@@ -114,6 +114,25 @@ def test_binding_refuses_host_tensors():
         fp8q.grouped_wgrad(c, s, c, s, torch.zeros(2, dtype=torch.int32))
 
 
+def test_sort_numbers_that_do_not_fit_are_refused_before_the_call(monkeypatch):
+    """ctypes keeps the low bits of a number that does not fit: none gets that far."""
+    class Lib:
+        @staticmethod
+        def fp8q_moe_sort_workspace(*_):
+            raise AssertionError("called")
+
+    monkeypatch.setattr(fp8q, "_lib", Lib)
+    monkeypatch.setattr(fp8q, "_rows_of", lambda t, name, dtypes: (2, 2, 2, 4096))
+    experts = torch.zeros((2, 2), dtype=torch.int32)
+    for bad in (dict(first=1 << 64), dict(first=(1 << 64) + 3), dict(first=1 << 31), dict(first=-1), dict(align=1 << 31), dict(align=1 << 32),
+                dict(align=0), dict(rows_cap=-1)):
+        with pytest.raises(ValueError):
+            fp8q.moe_sort(experts, 4, **bad)
+    for hosted in (-1, 1 << 31, (1 << 32) + 4):
+        with pytest.raises(ValueError):
+            fp8q.moe_sort(experts, hosted)
+
+
 def test_calls_run_on_the_tensors_own_device(monkeypatch):
     """With another device current the call is made under the tensors' device and on that device's stream."""
     seen, current = [], [0]
