@@ -18,7 +18,7 @@ struct __attribute__((packed, aligned(1))) Any8 {
 };
 
 // Eight BF16 values; those past `left` (which may be <= 0) are +0.  KEEP: a
-// plain load instead of a streaming one.
+// plain load instead of a streaming one (an unaligned load always is plain).
 template <bool KEEP = false>
 __device__ __forceinline__ uint4 ld_bf16x8(const uint16_t* p, int left, bool aligned) {
   if (left < 8) return load8_masked(p, left);

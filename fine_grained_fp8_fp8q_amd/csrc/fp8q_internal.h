@@ -105,7 +105,8 @@ hipError_t launch_moe_sort(const void* experts, bool i64, int pairs, int topk, i
 // MB of rows 27 against 34 us (float32 out 38 against 52), 112 MB 25 against
 // 23, 448 MB 95 against 88; combine backward of 59 MB 17.6 against 21.2, 117
 // MB 41 against 39; SwiGLU backward from 34 MB of cache and gradient 13.6
-// against 16.4, 67 MB 25.6 against 29.4, 134 MB 58 against 57.
+// against 16.4, 67 MB 25.6 against 29.4, 134 MB 58 against 57.  Rows off
+// 16-byte boundaries are always read with plain loads (chunk8.h).
 inline bool input_stays_cached(int64_t rows, int64_t row_bytes) {
   return row_bytes == 0 || rows <= ((int64_t)96 << 20) / row_bytes;
 }

@@ -221,6 +221,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
                                                       const int* __restrict__ row_of,
                                                       const float* __restrict__ weights, int topk, int chunks,
                                                       void* __restrict__ out, int64_t ldo) {
+  static_assert(VEC || KEEP, "loads of unaligned rows are plain ones");
   constexpr int W = OF32 ? 4 : 8, H = OF32 ? 2 : 1;  // columns of a load, loads of a row
   const int t = blockIdx.x / chunks;
   const int col0 = (blockIdx.x - t * chunks) * (int)blockDim.x * 8 + (int)threadIdx.x * W;
@@ -310,6 +311,7 @@ __device__ __forceinline__ void clear_row(uint8_t* p, int64_t bytes) {
 // without a pair.
 template <bool DF32, bool YF32, bool POW2, bool VEC, bool KEEP>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs a) {
+  static_assert(VEC || KEEP, "loads of unaligned rows are plain ones");
   __shared__ float part[4];
   const int tid = threadIdx.x;
   const int nb = (a.n + 127) >> 7;
@@ -411,6 +413,16 @@ static void with_flag(bool flag, F f) {
   }
 }
 
+// f(VEC, KEEP): rows that are not VEC are loaded one way only.
+template <class F>
+static void with_load(bool vec, bool keep, F f) {
+  if (vec) {
+    with_flag(keep, [&](auto kept) { f(std::true_type{}, kept); });
+  } else {
+    f(std::false_type{}, std::true_type{});
+  }
+}
+
 hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t ldy, const int* row_of,
                               const float* weights, int tokens, int topk, bool out_f32, void* out, int64_t ldo,
                               hipStream_t stream) {
@@ -418,13 +430,11 @@ hipError_t launch_moe_combine(const void* y, bool y_f32, int cap, int n, int64_t
   const int chunks = (items + threads - 1) / threads;
   const dim3 grid((unsigned)(tokens * chunks)), block(threads);
   const bool keep = input_stays_cached(cap, ldy * (y_f32 ? 4 : 2));
-  with_flag(n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0, [&](auto vec) {
-    with_flag(keep, [&](auto kept) {
-      constexpr bool V = decltype(vec)::value, K = decltype(kept)::value;
-      auto kernel = y_f32 ? (out_f32 ? combine_kernel<true, true, V, K> : combine_kernel<true, false, V, K>)
-                          : (out_f32 ? combine_kernel<false, true, V, K> : combine_kernel<false, false, V, K>);
-      hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo);
-    });
+  with_load(n % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0, keep, [&](auto vec, auto kept) {
+    constexpr bool V = decltype(vec)::value, K = decltype(kept)::value;
+    auto kernel = y_f32 ? (out_f32 ? combine_kernel<true, true, V, K> : combine_kernel<true, false, V, K>)
+                        : (out_f32 ? combine_kernel<false, true, V, K> : combine_kernel<false, false, V, K>);
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, y, cap, n, ldy, row_of, weights, topk, chunks, out, ldo);
   });
   return hipGetLastError();
 }
@@ -441,14 +451,12 @@ hipError_t launch_moe_combine_backward(const void* dout, bool dout_f32, int toke
   const bool whole = n % 8 == 0 && lddo % 8 == 0 && (!y || ldy % 8 == 0) && (!dy || lddy % 8 == 0) && (!codes || ldc % 8 == 0);
   const int zero = token && (dy || codes) ? (cap + kZeroRows - 1) / kZeroRows : 0;
   const dim3 grid(a.pairs + zero), block(combine_backward_threads(a.pairs, n));
-  with_flag(whole, [&](auto vec) {
-    with_flag(y && input_stays_cached(cap, ldy * (y_f32 ? 4 : 2)), [&](auto kept) {
-      with_flag(pow2, [&](auto p2) {
-        constexpr bool V = decltype(vec)::value, K = decltype(kept)::value, P = decltype(p2)::value;
-        auto kernel = dout_f32 ? (y_f32 ? combine_bwd_kernel<true, true, P, V, K> : combine_bwd_kernel<true, false, P, V, K>)
-                               : (y_f32 ? combine_bwd_kernel<false, true, P, V, K> : combine_bwd_kernel<false, false, P, V, K>);
-        hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
-      });
+  with_load(whole, y && input_stays_cached(cap, ldy * (y_f32 ? 4 : 2)), [&](auto vec, auto kept) {
+    with_flag(pow2, [&](auto p2) {
+      constexpr bool V = decltype(vec)::value, K = decltype(kept)::value, P = decltype(p2)::value;
+      auto kernel = dout_f32 ? (y_f32 ? combine_bwd_kernel<true, true, P, V, K> : combine_bwd_kernel<true, false, P, V, K>)
+                             : (y_f32 ? combine_bwd_kernel<false, true, P, V, K> : combine_bwd_kernel<false, false, P, V, K>);
+      hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
     });
   });
   return hipGetLastError();

@@ -69,6 +69,7 @@ __device__ __forceinline__ void widen8(uint4 c, float scale, float* v) {
 // tiles' loads in flight takes 124.
 template <bool CACHE, bool QUANT, bool POW2, bool VEC, bool KEEP>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwdArgs a) {
+  static_assert(VEC || KEEP, "loads of unaligned rows are plain ones");
   const int lane = threadIdx.x & 63;
   const int sub = lane & 15;
   const uint32_t t = ((blockIdx.x * 256u + threadIdx.x) >> 6) * 4u + (uint32_t)(lane >> 4);
