@@ -268,6 +268,46 @@ def test_combine_backward_empty():
     assert not host(fp8q.moe_combine_backward(z(3, 40), z(0, 40), none)[3]).any()
 
 
+@pytest.mark.parametrize("ddt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("ydt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [1, 7, 16, 520, 1027])
+def test_combine_backward_non_finite_values(ddt, ydt, n):
+    """Infinities and NaN in dout, y and the weights follow float32 arithmetic in the BF16 rows and in the weights'
+    gradient; those of pairs without a row and of rows without a pair reach nothing."""
+    r = np.random.default_rng(n)
+    tokens, topk, cap = 8, 3, 40
+    row_of = r.permutation(cap)[:tokens * topk].reshape(tokens, topk).astype(np.int32)
+    row_of[1, 0], row_of[5, 2], row_of[6] = -1, cap, [2 ** 31 - 1, -2 ** 31, -7]
+    has = (row_of >= 0) & (row_of < cap)
+    token = np.full(cap, -1, dtype=np.int32)
+    token[row_of[has]] = np.nonzero(has)[0]
+    dv, yv = f64(bf16(r, (tokens, n))), f64(bf16(r, (cap, n)))
+    w = r.random(size=(tokens, topk)).astype(np.float32)
+    yv[row_of[7], 0] = 0.5  # (their products with 2^127 below stay finite)
+    dv[0, n // 2], dv[2, 0], dv[3, n - 1], dv[6] = np.inf, np.nan, -np.inf, np.nan
+    yv[row_of[4, 0], n - 1], yv[row_of[4, 1], 0], yv[row_of[7, 2], n // 3], yv[token < 0] = np.inf, np.nan, -np.inf, np.nan
+    yv[row_of[3, 1], n - 1] = 0.0  # against an infinity of dout
+    w[1, 0], w[4, 2], w[5, 0], w[7, 0], w[0, 1], w[6] = np.nan, np.inf, np.nan, -np.inf, 0.0, np.inf
+    dv[7, 0] = 2.0 ** 127  # finite, and 2^127 times 3 is not
+    w[7, 1] = 3.0
+    y, dout = torch.from_numpy(yv).to("cuda:0").to(ydt), torch.from_numpy(dv).to("cuda:0").to(ddt)
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = np.zeros((cap, n), dtype=np.float32)
+        for t, j in zip(*np.nonzero(has)):
+            want[row_of[t, j]] = w[t, j] * dv[t].astype(np.float32)
+        terms = np.where(has[:, :, None], dv[:, None, :] * yv[np.where(has, row_of, 0)], 0.0)
+        want_dw = terms.sum(2)
+    bound = 1.01 * (8 * (-(-n // 512)) + 10) * U32 * np.abs(np.where(np.isfinite(terms), terms, 0.0)).sum(2) + 2.0 ** -149
+    for pad in (0, 5):
+        dy, _, _, dw = fp8q.moe_combine_backward(spread(dout, pad, 3.0), spread(y, pad, 3.0), dev(row_of), dev(w), dev(token))
+        assert np.array_equal(host(dy.float()), host(torch.from_numpy(want).bfloat16().float()), equal_nan=True), pad
+        dw = host(dw).astype(np.float64)
+        fin = np.isfinite(want_dw)
+        assert np.array_equal(dw[~fin], want_dw[~fin], equal_nan=True), pad
+        assert_near(dw[fin], want_dw[fin], bound[fin], "dweights")
+        assert (dw[~has] == 0).all()
+
+
 @pytest.mark.parametrize("tokens", [1, 3, 1024, 1025])
 def test_combine_backward_of_rows_without_columns(tokens):
     """The weight gradients of an empty width are zeros, on both sides of 2048 pairs."""
@@ -387,6 +427,30 @@ def test_grouped_wgrad(acc, mode, nout, kin, sizes):
     assert torch.equal(odd[:, :, :kin], got) and (odd[:, :, kin:] == 5).all()
 
 
+# (kin 8208: enough 256 x 256 tiles for the forms that the matrix core accumulates; 4112: 128 x 128; the others 64 x 64)
+@pytest.mark.parametrize("acc,mode", [("fp32", "free"), ("fp32_pow2", "pow2"), ("fp8_mfma", "free"), ("fp8_mfma_scaled", "pow2")])
+@pytest.mark.parametrize("nout,kin,sizes", [(40, 80, [130, 0, 1]), (300, 272, [700, 65]), (129, 16, [128]), (2000, 4112, [700, 400]), (2000, 8208, [900, 700])])
+def test_grouped_wgrad_of_partial_tiles_on_line_boundaries(acc, mode, nout, kin, sizes):
+    """Row strides of whole 64-byte lines (streaming stores) with tiles that end inside a row and a column: nothing is
+    written past the columns, nor past the last row."""
+    r = np.random.default_rng(kin)
+    padded = [-(-s // 128) * 128 for s in sizes]
+    offsets = np.concatenate([[0], np.cumsum(padded)]).astype(np.int32)
+    real = np.zeros(int(offsets[-1]), bool)
+    for s, o in zip(sizes, offsets):
+        real[o:o + s] = True
+    d = [dev(v) for v in (*token_operand(r, nout, real.size, real, mode), *token_operand(r, kin, real.size, real, mode), offsets)]
+    for ld in (kin, kin + 16):
+        buf = torch.full((len(sizes) * nout + 64, ld), 5.0, device="cuda:0")
+        out = buf[:len(sizes) * nout].view(len(sizes), nout, ld)[:, :, :kin]
+        fp8q.grouped_wgrad(*d, out=out, acc=acc)
+        for g, (a, b) in enumerate(zip(offsets[:-1], offsets[1:])):
+            alone = fp8q.wgrad(d[0][:, a:b].contiguous(), d[1][:, a // 128:b // 128].contiguous(), d[2][:, a:b].contiguous(),
+                               d[3][:, a // 128:b // 128].contiguous(), acc=acc) if b > a else torch.zeros((nout, kin), device="cuda:0")
+            assert torch.equal(out[g], alone), f"group {g}, stride {ld}"
+        assert (buf[:len(sizes) * nout, kin:] == 5).all() and (buf[len(sizes) * nout:] == 5).all()
+
+
 def test_grouped_wgrad_broken_tables_stay_inside():
     """Offsets outside the rows, decreasing or off the tiles are clamped and rounded down (a precondition the
     kernel does not report); the answers are those of the clamped table."""
@@ -408,6 +472,40 @@ def test_grouped_wgrad_empty():
     off = torch.zeros(4, dtype=torch.int32, device="cuda:0")
     assert not host(fp8q.grouped_wgrad(c, s, c, s, off)).any()
     assert fp8q.grouped_wgrad(c, s, c, s, off[:1]).shape == (0, 8, 8)
+
+
+@pytest.mark.parametrize("n", [1, 5, 128, 300])
+def test_single_columns_of_any_column_stride(n):
+    """A tensor of one column has no column stride to speak of: every call with row-major operands takes it, and answers as
+    for the contiguous one."""
+    r = np.random.default_rng(n)
+    col = dev_bf16(bf16(r, (n, 1)))
+    odd = dev_bf16(bf16(r, (n, 3)))
+    odd[:, :1] = col
+    views = [col.t().contiguous().t(), torch.as_strided(col, (n, 1), (1, 77)), torch.as_strided(odd, (n, 1), (3, 2))]
+    assert all(v.shape == (n, 1) and torch.equal(v, col) for v in views) and views[1].stride(1) == 77
+
+    def same(call):
+        want = call(col)
+        for v in views:
+            got = call(v)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    same(lambda v: fp8q.quantize_act(v))
+    same(lambda v: fp8q.quantize_act(v, "token_t", "pow2"))
+    same(lambda v: fp8q.quantize_weight(v))
+    same(lambda v: fp8q.quantize_weight_t(v))
+    same(lambda v: fp8q.quantize_linear(v, v))
+    index = torch.arange(n, dtype=torch.int32, device="cuda:0").flip(0).contiguous()
+    codes, scales = fp8q.quantize_act(col)
+    want = fp8q.gather_rows(codes.contiguous(), scales, index)
+    for v in (codes, torch.as_strided(codes.contiguous(), (n, 1), (1, 9))):
+        assert all(torch.equal(a, b) for a, b in zip(fp8q.gather_rows(v, scales, index), want))
+    rows = index[:, None].contiguous()
+    same(lambda v: (fp8q.moe_combine(v, rows),))
+    same(lambda v: fp8q.moe_combine_backward(v, v, rows)[::3])
+    both = torch.cat([col, col], 1)
+    same(lambda v: fp8q.swiglu_backward(both, v)[:1])
 
 
 def test_refusals_of_the_binding():
