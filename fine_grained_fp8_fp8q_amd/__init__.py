@@ -562,11 +562,12 @@ def _types():
 
 def _pair_table(row_of, weights):
     """Checks row_of and weights: contiguous [tokens, topk]."""
-    shape = row_of.shape
-    if row_of.dtype != _types()[2] or len(shape) != 2 or not row_of.is_contiguous():
-        _need(row_of, _types()[2], "row_of")
+    tensor, (f32, _), i32 = _types()
+    if not isinstance(row_of, tensor) or row_of.dtype != i32 or row_of.dim() != 2 or not row_of.is_contiguous():
+        _need(row_of, i32, "row_of")
         raise ValueError("row_of must be a contiguous int32 [tokens, topk] tensor")
-    if weights is not None and (weights.dtype != _types()[1][0] or weights.shape != shape or
+    shape = row_of.shape
+    if weights is not None and (not isinstance(weights, tensor) or weights.dtype != f32 or weights.shape != shape or
                                 not weights.is_contiguous()):
         _contig_f32(weights, "weights")
         raise ValueError("weights must have the shape of row_of")
@@ -622,16 +623,17 @@ def moe_combine(y, row_of, weights=None, out_dtype=None, out=None):
     types = _types()[1]
     cap, n, ld, y_p = _rows_of(y, "y", types)
     tokens, topk = _pair_table(row_of, weights)
-    dev = _one_device(y, row_of, weights, out)
     if out is None:
+        dev = _one_device(y, row_of, weights)
         out_dtype = out_dtype or types[OUT_BF16]
         if out_dtype not in types:
             raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
         out, ldo = _new(tokens, n, out_dtype, dev), max(n, 1)
     else:
+        ot, on, ldo, _ = _rows_of(out, "out", types)
+        dev = _one_device(y, row_of, weights, out)
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out has another type than out_dtype")
-        ot, on, ldo, _ = _rows_of(out, "out", types)
         if (ot, on) != (tokens, n):
             raise ValueError(f"out must be [{tokens}, {n}], got [{ot}, {on}]")
     _call(dev, "fp8q_moe_combine", y_p, types.index(y.dtype), cap, n, ld, _addr(row_of), _addr(weights), tokens, topk,
@@ -656,7 +658,8 @@ def moe_combine_backward(dout, y, row_of, weights=None, token=None, bf16=True, q
     if (dt, dn) != (tokens, n):
         raise ValueError(f"dout must be [{tokens}, {n}], got [{dt}, {dn}]")
     if token is not None:
-        if token.dtype != torch.int32 or token.shape != (cap,) or not token.is_contiguous():
+        if not isinstance(token, torch.Tensor) or token.dtype != torch.int32 or token.shape != (cap,) or \
+                not token.is_contiguous():
             _need(token, torch.int32, "token")
             raise ValueError(f"token must be a contiguous int32 tensor of {cap} rows")
     dev = _one_device(y, dout, row_of, weights, token)
@@ -732,8 +735,8 @@ def grouped_wgrad(dy_t, dy_scales, x_t, x_scales, offsets, out=None, acc="fp32")
         raise ValueError("scales must be [rows of the codes, tokens/128]")
     if cap and (ld0, ld1, ld2, ld3) != (cap, cap, nb, nb):
         raise ValueError("codes and scales must be contiguous")
-    if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.dim() != 1 or not offsets.is_contiguous() or \
-            not offsets.numel():
+    if not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int32 or not offsets.is_cuda or \
+            offsets.dim() != 1 or not offsets.is_contiguous() or not offsets.numel():
         _need(offsets, torch.int32, "offsets")
         raise ValueError("offsets must be a contiguous int32 [G+1] tensor")
     g = offsets.numel() - 1

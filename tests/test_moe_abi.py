@@ -133,6 +133,28 @@ def test_sort_numbers_that_do_not_fit_are_refused_before_the_call(monkeypatch):
             fp8q.moe_sort(experts, hosted)
 
 
+def test_binding_refuses_what_is_no_tensor(monkeypatch):
+    """Lists in the place of any tensor, next to operands that pass, are a TypeError that names the argument."""
+    def rows_of(t, name, dtypes, checked=fp8q._rows_of):
+        return (*t.shape, t.shape[1], 4096) if isinstance(t, torch.Tensor) else checked(t, name, dtypes)
+
+    monkeypatch.setattr(fp8q, "_rows_of", rows_of)
+    y, rows, w = torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))
+    c, s, off = torch.zeros((4, 128), dtype=torch.uint8), torch.zeros((4, 1)), torch.zeros(2, dtype=torch.int32)
+    for name, call in (("row_of", lambda: fp8q.moe_combine(y, rows.tolist())), ("weights", lambda: fp8q.moe_combine(y, rows, w.tolist())),
+                       ("out", lambda: fp8q.moe_combine(y, rows, out=y.tolist())),
+                       ("out", lambda: fp8q.moe_combine(y, rows, out=y.tolist(), out_dtype=torch.float32)),
+                       ("y", lambda: fp8q.moe_combine(y.tolist(), rows)), ("experts", lambda: fp8q.moe_sort(rows.tolist(), 4)),
+                       ("dout", lambda: fp8q.moe_combine_backward(y.tolist(), y, rows)),
+                       ("row_of", lambda: fp8q.moe_combine_backward(y, y, rows.tolist())),
+                       ("token", lambda: fp8q.moe_combine_backward(y, y, rows, w, off.tolist())),
+                       ("dy", lambda: fp8q.swiglu_backward(y, y[:, :4].tolist())),
+                       ("x_scales", lambda: fp8q.swiglu_backward(torch.zeros((4, 256)), torch.zeros((4, 128)), x_scales=s.tolist())),
+                       ("offsets", lambda: fp8q.grouped_wgrad(c, s, c, s, off.tolist()))):
+        with pytest.raises(TypeError, match=name):
+            call()
+
+
 def test_calls_run_on_the_tensors_own_device(monkeypatch):
     """With another device current the call is made under the tensors' device and on that device's stream."""
     seen, current = [], [0]
