@@ -385,6 +385,58 @@ def test_swiglu_backward_against_differences():
     assert_near(dx, diff, U16 * np.abs(diff) + M.SWIGLU_BWD_REL * mag + 1e-9 * (np.abs(dy * u).repeat(1, 0) @ np.ones((128, 256)) + 1), "dx")
 
 
+def test_swiglu_backward_empty():
+    for rows, inter in ((0, 128), (5, 0), (0, 0)):
+        x = torch.zeros((rows, 2 * inter), dtype=torch.bfloat16, device="cuda:0")
+        dy = torch.zeros((rows, inter), dtype=torch.bfloat16, device="cuda:0")
+        scales = torch.zeros((rows, 2 * inter // 128), device="cuda:0")
+        for xx, ss in ((x, None), (x.to(torch.uint8), scales)):
+            dx, y, codes, dxs = fp8q.swiglu_backward(xx, dy, x_scales=ss, quantize=True, want_y=True)
+            assert dx.shape == codes.shape == (rows, 2 * inter) and y.shape == (rows, inter) and dxs.shape == scales.shape
+
+
+@pytest.mark.parametrize("pads", [(8, 8, 16), (3, 1, 5), (0, 8, 1)])
+def test_outputs_of_any_row_stride_leave_the_gaps_alone(pads):
+    """Rows further apart than their length, on and off 16-byte boundaries, for every output of the two gradients."""
+    lib, stream = fp8q.load_library(), torch.cuda.current_stream().cuda_stream
+    r = np.random.default_rng(sum(pads))
+
+    def buffer(rows, cols, pad, dtype):
+        return torch.full((rows, cols + pad), 9, dtype=dtype, device="cuda:0")
+
+    def check(buf, want, what):
+        n = want.shape[1]
+        assert torch.equal(buf[:, :n], want) and (buf[:, n:] == 9).all(), what
+
+    for n, inter in ((1030, 256), (640, 128)):
+        dout, y = dev_bf16(bf16(r, (40, n))), dev_bf16(bf16(r, (50, n)))
+        row_of = r.permutation(50)[:40].reshape(40, 1).astype(np.int32)
+        row_of[::9] = -1
+        token = np.full(50, -1, dtype=np.int32)
+        token[row_of[row_of >= 0]] = np.nonzero(row_of >= 0)[0]
+        rows, tok, w = dev(row_of), dev(token), torch.rand((40, 1), device="cuda:0")
+        dy, codes, scales, dw = fp8q.moe_combine_backward(dout, y, rows, w, tok, quantize=True)
+        b_dy, b_codes = buffer(50, n, pads[0], torch.bfloat16), buffer(50, n, pads[1], torch.uint8)
+        b_s, b_dw = torch.full_like(scales, 9.0), torch.full_like(dw, 9.0)
+        assert lib.fp8q_moe_combine_backward(dout.data_ptr(), 1, 40, n, n, y.data_ptr(), 1, 50, n, rows.data_ptr(), w.data_ptr(), 1, tok.data_ptr(),
+                                             b_dy.data_ptr(), n + pads[0], 0, b_codes.data_ptr(), n + pads[1], b_s.data_ptr(), b_dw.data_ptr(),
+                                             stream) == fp8q.OK
+        check(b_dy, dy, "dy")
+        check(b_codes, codes, "codes")
+        assert torch.equal(b_s, scales) and torch.equal(b_dw, dw)
+        x, g = dev_bf16(bf16(r, (30, 2 * inter))), dev_bf16(bf16(r, (30, inter)))
+        dx, out, codes, scales = fp8q.swiglu_backward(x, g, quantize=True, want_y=True)
+        b_dx, b_codes = buffer(30, 2 * inter, pads[0], torch.bfloat16), buffer(30, 2 * inter, pads[1], torch.uint8)
+        b_y, b_s = buffer(30, inter, pads[2], torch.bfloat16), torch.full_like(scales, 9.0)
+        assert lib.fp8q_swiglu_backward(x.data_ptr(), None, 30, inter, 2 * inter, g.data_ptr(), inter, b_dx.data_ptr(), 2 * inter + pads[0],
+                                        fp8q.SCALE_POW2, b_codes.data_ptr(), 2 * inter + pads[1], b_s.data_ptr(), b_y.data_ptr(),
+                                        inter + pads[2], stream) == fp8q.OK
+        check(b_dx, dx, "dx")
+        check(b_codes, codes, "dx codes")
+        check(b_y, out, "y")
+        assert torch.equal(b_s, scales)
+
+
 # --------------------------------------------------------- grouped wgrad ----
 
 def token_operand(r, width, cap, real, mode, std=1.0):
@@ -472,6 +524,13 @@ def test_grouped_wgrad_empty():
     off = torch.zeros(4, dtype=torch.int32, device="cuda:0")
     assert not host(fp8q.grouped_wgrad(c, s, c, s, off)).any()
     assert fp8q.grouped_wgrad(c, s, c, s, off[:1]).shape == (0, 8, 8)
+
+
+def test_grouped_wgrad_without_outputs():
+    c, s = torch.zeros((8, 256), dtype=torch.uint8, device="cuda:0"), torch.zeros((8, 2), device="cuda:0")
+    off = torch.tensor([0, 128, 256], dtype=torch.int32, device="cuda:0")
+    assert fp8q.grouped_wgrad(c[:0], s[:0], c, s, off).shape == (2, 0, 8)
+    assert fp8q.grouped_wgrad(c, s, c[:0], s[:0], off).shape == (2, 8, 0)
 
 
 @pytest.mark.parametrize("n", [1, 5, 128, 300])
