@@ -22,9 +22,10 @@
 //     16 rows, or the fullest group with the emptiest), a persistent grid with
 //     the next tile's loads under the last block of this one, both blocks of a
 //     short loop loaded at once: no faster (452-482, 451-459, 453-517, 433
-//     against 433 us), not kept.
+//     against 433 us), not kept.  (All on 128 x 128 tiles with the folded
+//     form: a persistent grid of 256 x 256 tiles was not tried.)
 // What bounds it now: the writes take 332 us alone and the products 326 us
-// alone; together the power and the memory they share give 433-454.
+// alone; together the power and the memory they share give 433-459.
 #include <type_traits>
 
 #include "fp8q_internal.h"
@@ -393,8 +394,13 @@ void launch(WgArgs g, int groups, int acc, hipStream_t stream) {
   // L2: of the ways to lay eight regions over the tiles, the one with the
   // smallest border.  (7168 x 2048, 16 groups: 8192 rows 319 -> 282 us and
   // 32768 rows 846 -> 816 us against eight regions side by side, 256 x 256
-  // tiles, power-of-two float32 form; nothing to gain or lose within 2% where
-  // the writes decide.)
+  // tiles, power-of-two float32 form, and 998 MB read instead of 2523; within
+  // 2% either way for 4096 x 7168, where the writes decide.)  Both divide into
+  // even regions.  Balance is not looked at: where tiles do not divide, the
+  // same XCDs have more than their share in every group (128 x 128 tiles of
+  // 1152 x 640 and 1100 x 1100: the fullest 1.60 and 1.48 times the mean and
+  // two without work; 2816 x 2048, 2880 x 2880: 1.09; 64 x 64 tiles of 320 x
+  // 320: 1.92), not measured against another layout.
   int best = 0;
   for (int xn = 1; xn <= 8; xn *= 2) {
     const int xm = 8 / xn, rm = (g.tiles_m + xm - 1) / xm, rn = (g.tiles_n + xn - 1) / xn;
@@ -427,27 +433,28 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
   // tiles of 128 x 128 than three quarters of the units, or, as groups are
   // uneven and the fullest is the last, fewer than half of them in a group and
   // five for every two in all.  Groups x outputs, rows in all, float32 form,
-  // against 128 x 128: 1 x 512 x 512, 16384 rows 65 and 156 us; 4 x 512 x 512,
-  // 4096 rows 12.1 and 25.6; 8 x 1024 x 1024, 16384 rows 46 and 67; 16 x 768 x
-  // 768 (576 tiles), 16384 rows 39 and 56; past the rule 1 x 2048 x 2048, 16384
-  // rows 172 and 158, 16 x 1024 x 1024 (1024 tiles), 4096 rows 22.9 and 20.1.
+  // against 128 x 128: 1 x 512 x 512, 16384 rows 65 and 155 us; 4 x 512 x 512,
+  // 4096 rows 12.9 and 26.3; 8 x 1024 x 1024, 16384 rows 51 and 74; 16 x 768 x
+  // 768 (576 tiles), 16384 rows 39 and 59; past the rule 1 x 2048 x 2048, 16384
+  // rows 172 and 161, 16 x 1024 x 1024 (1024 tiles), 4096 rows 24.3 and 21.1.
   // (Four K blocks in flight instead of two, or eight waves a tile: nothing
-  // gained.)
+  // gained.)  One workgroup walks all blocks of its tile, 0.5 us each: with few
+  // tiles that, and not a rate, is the time.
   //
   // Forms that accumulate in the matrix core need half the vector work per
   // product on 256 x 256 tiles (a W fragment is widened for 64 rows either
   // way, an A fragment for 128 columns instead of 64).  That pays once a tile
   // has enough blocks to hide that a compute unit holds one such tile and not
   // two, and there are tiles for all units: 4096 x 7168, 16 groups,
-  // power-of-two float32 form, 2.5 / 4.6 / 8.7 blocks a group: 421 / 578 / 883
-  // us against 403 / 602 / 946 on 128 x 128; 7168 x 2048, 16.6 blocks: 824
-  // against 910 (hardware scales: 606 against 718).  Groups are uneven: of
-  // several the fullest alone has to keep a quarter of the units busy, and all
-  // of them two tiles for each (16 x 1024 x 2048, 16384 rows: 111 against 77
-  // us; 4 x 2048 x 2048, 4096 rows: 53 against 43; 16 x 2048 x 2048, 8192 rows:
-  // 88 against 93; one group of 4096 x 4096, 4096 rows: 103 against 121).  The
-  // folded form is VALU-bound on either (1112 against 1062 us at 8.7 blocks)
-  // and spills on the large one.
+  // power-of-two float32 form, 2.4 / 4.5 / 8.6 blocks a group: 424 / 631 / 951
+  // us against 410 / 690 / 1050 on 128 x 128; 7168 x 2048, 16.6 blocks: 811
+  // against 917 (hardware scales: 551 against 711, FP8 partials 688 against
+  // 744).  Groups are uneven: of several the fullest alone has to keep a
+  // quarter of the units busy, and all of them two tiles for each (16 x 1024 x
+  // 2048, 16384 rows: 111 against 78 us; 4 x 2048 x 2048, 4096 rows: 52 against
+  // 42; 16 x 2048 x 2048, 8192 rows: 84 against 85; one group of 4096 x 4096,
+  // 4096 rows: 102 against 115).  The folded form is VALU-bound on either (1112
+  // against 1062 us at 8.6 blocks) and spills on the large one.
   const auto tiles = [&](int t) { return (int64_t)((nout + t - 1) / t) * ((kin + t - 1) / t) * groups; };
   const int cus = device_cus();
   const bool fills = groups == 1 ? tiles(256) >= cus : tiles(256) >= 2 * cus && 4 * tiles(256) >= (int64_t)cus * groups;

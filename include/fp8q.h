@@ -391,8 +391,9 @@ fp8q_status fp8q_moe_combine(const void* y, int y_dtype, int64_t rows_cap, int64
  * activation gradient before the down-projections takes power-of-two
  * scales); dy_bf16, dy_codes and dweights may each be NULL (then that output
  * is not formed; y is read only for dweights and may be NULL without it).
- * weights NULL means 1 everywhere.  Pairs without a row in [0, rows_cap) get
- * dweights 0.  token [rows_cap] is fp8q_moe_sort's: rows whose token is
+ * weights NULL means 1 everywhere.  Pairs without a row in [0, rows_cap), and
+ * with N = 0 all, get dweights 0.  Non-finite values of dout, y and weights
+ * follow float32 arithmetic in dy_bf16 and dweights.  token [rows_cap] is fp8q_moe_sort's: rows whose token is
  * negative (padding and everything behind the last group) are written as
  * zero values, codes and scales; with token NULL rows that no pair names are
  * left as they were.  No two pairs may name the same row.  For the quantized
