@@ -31,6 +31,11 @@ Functions (names follow the C ABI without the ``fp8q_`` prefix):
   ``moe_combine`` / ``moe_combine_backward`` (weighted sum of a token's
   expert rows and its gradient), ``swiglu_backward`` (from the BF16 input or
   its FP8 cache) and ``grouped_wgrad`` (every expert's weight gradient)
+* between a block's linear layers: ``rmsnorm_quantize`` (residual addition,
+  RMS norm and 1x128 quantization), ``rmsnorm_backward``,
+  ``rmsnorm_quantize_t`` (the normalised rows in token-axis tiles, by a routing
+  table's token list if given), ``moe_route`` (the router's choice of experts)
+  and ``moe_route_backward``
 """
 
 import ctypes
@@ -45,11 +50,15 @@ OUT_F32, OUT_BF16 = 0, 1
 ACC_FP32, ACC_FP8_MFMA, ACC_FP8_MFMA_SCALED, ACC_FP32_POW2 = 0, 1, 2, 3
 TILE_ROW, TILE_TOKEN_T = 0, 1
 INDEX_I32, INDEX_I64 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP_TWO = 0, 1
 
 SYMBOLS = ("fp8q_quantize_act", "fp8q_quantize_weight", "fp8q_quantize_linear", "fp8q_quantize_weight_t", "fp8q_gemm",
            "fp8q_gemm_ex", "fp8q_gemm_quantized", "fp8q_grouped_gemm", "fp8q_grouped_gemm_ex", "fp8q_wgrad",
            "fp8q_wgrad_ex", "fp8q_gather_rows", "fp8q_swiglu_quantize", "fp8q_moe_sort", "fp8q_moe_combine",
            "fp8q_moe_combine_backward", "fp8q_swiglu_backward", "fp8q_grouped_wgrad", "fp8q_grouped_wgrad_ex",
+           "fp8q_rmsnorm_quantize", "fp8q_rmsnorm_backward", "fp8q_rmsnorm_quantize_t", "fp8q_moe_route",
+           "fp8q_moe_route_backward", "fp8q_rmsnorm_backward_workspace",
            "fp8q_moe_sort_workspace", "fp8q_set_gemm_small_limit", "fp8q_status_string")
 
 _lib = None
@@ -91,11 +100,20 @@ def load_library(path=None):
     lib.fp8q_swiglu_backward.argtypes = [vp, vp, i64, i64, i64, vp, i64, vp, i64, ip, vp, i64, vp, vp, i64, vp]
     lib.fp8q_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, i64, vp]
     lib.fp8q_grouped_wgrad_ex.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, ip, vp, i64, vp]
+    f64 = ctypes.c_double
+    lib.fp8q_rmsnorm_quantize.argtypes = [vp, ip, i64, i64, i64, vp, ip, i64, vp, i64, vp, ip, f64, vp, i64, ip, vp, i64, vp, vp, vp]
+    lib.fp8q_rmsnorm_backward.argtypes = [vp, ip, i64, i64, i64, vp, ip, i64, vp, vp, ip, vp, i64, vp, ip, i64, ip, vp, i64, vp, vp,
+                                          vp, i64, vp]
+    lib.fp8q_rmsnorm_quantize_t.argtypes = [vp, ip, i64, i64, i64, vp, vp, ip, vp, i64, ip, vp, i64, vp, vp]
+    lib.fp8q_moe_route.argtypes = [vp, ip, i64, i64, i64, vp, ip, i32, i32, ip, i64, ip, f64, ip, vp, vp, vp, vp, vp]
+    lib.fp8q_moe_route_backward.argtypes = [vp, vp, ip, i64, i64, vp, ip, i64, i64, ip, ip, f64, vp, vp, ip, i64, vp]
+    lib.fp8q_rmsnorm_backward_workspace.argtypes = [i64, i64]
+    lib.fp8q_rmsnorm_backward_workspace.restype = i64
     lib.fp8q_moe_sort_workspace.argtypes = [i64, i64, i32]
     lib.fp8q_moe_sort_workspace.restype = i64
     lib.fp8q_set_gemm_small_limit.argtypes = [i64]
     lib.fp8q_set_gemm_small_limit.restype = i64
-    for name in SYMBOLS[:-3]:
+    for name in SYMBOLS[:-4]:
         getattr(lib, name).restype = ctypes.c_int
     lib.fp8q_status_string.argtypes = [ctypes.c_int]
     lib.fp8q_status_string.restype = ctypes.c_char_p
@@ -760,3 +778,212 @@ def grouped_wgrad(dy_t, dy_scales, x_t, x_scales, offsets, out=None, acc="fp32")
     else:
         _call(dev, "fp8q_grouped_wgrad_ex", *args, code, _addr(dw), ldw)
     return dw
+
+
+# ------------------------------------- between a block's linear layers ----
+
+def _vector(t, n, dtypes, name):
+    """Address of a contiguous GPU vector of n elements and one of the types given."""
+    if not isinstance(t, _types()[0]):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+    return t.data_ptr()
+
+
+def rmsnorm_quantize(x, weight, residual=None, eps=1e-6, bf16=False, quantize=True, scale_mode="free", h_out=None):
+    """Residual addition, RMS norm and 1x128 quantization of its output.
+
+    x BF16 or float32 [rows, N], weight BF16 or float32 [N].  With a residual
+    (BF16 or float32 [rows, N]) h = x + residual is rounded to its type and
+    normalised, without one x is.  Returns (y, codes, scales, rstd, h), None
+    for what was not asked for: y BF16 [rows, N] (bf16=True), its codes and
+    scales (quantize=True), rstd = 1 / rms float32 [rows], and h like residual
+    (None without one), written to h_out if given, which may be residual
+    itself.
+    """
+    torch = _torch()
+    f32, b16 = types = _types()[1]
+    rows, n, ldx, x_p = _rows_of(x, "x", types)
+    w_p = _vector(weight, n, types, "weight")
+    h, res_p, ldr, ldh, stream = None, None, n, n, OUT_BF16
+    if residual is not None:
+        rr, rn, ldr, res_p = _rows_of(residual, "residual", types)
+        if (rr, rn) != (rows, n):
+            raise ValueError(f"residual must be [{rows}, {n}], got [{rr}, {rn}]")
+        stream = types.index(residual.dtype)
+        if h_out is not None:
+            hr, hn, ldh, _ = _rows_of(h_out, "h_out", (residual.dtype,))
+            if (hr, hn) != (rows, n):
+                raise ValueError(f"h_out must be [{rows}, {n}], got [{hr}, {hn}]")
+            h = h_out
+    elif h_out is not None:
+        raise ValueError("h_out goes with a residual")
+    dev = _one_device(x, weight, residual, h_out)
+    if residual is not None and h is None:
+        h = _new(rows, n, residual.dtype, dev)
+    y = _new(rows, n, b16, dev) if bf16 else None
+    codes = scales = None
+    ldc = n
+    if quantize:
+        codes, ldc = _new_codes(rows, n, dev)
+        scales = _new(rows, (n + 127) // 128, f32, dev)
+    rstd = torch.empty_strided((rows,), (1,), dtype=f32, device=dev)
+    _call(dev, "fp8q_rmsnorm_quantize", x_p, types.index(x.dtype), rows, n, ldx, res_p, stream, ldr, _addr(h), ldh, w_p,
+          types.index(weight.dtype), eps, _addr(y), n, _scale_mode(scale_mode), _addr(codes), ldc, _addr(scales), _addr(rstd))
+    return y, codes, scales, rstd, h
+
+
+def rmsnorm_backward(dy, h, rstd, weight, dres=None, out_dtype=None, quantize=False, scale_mode="free", want_dx=True, want_dweight=True):
+    """Gradient of the norm for dy (BF16 or float32 [rows, N]), from the h it
+    normalised (x without a residual), rstd and weight of ``rmsnorm_quantize``.
+
+    dres, the gradient that reaches h past the norm, is added to dx and has
+    its type out_dtype (torch.bfloat16 by default, dres's type with one).
+    Returns (dx, codes, scales, dweight), None for what was not asked for: dx
+    [rows, N] (want_dx), the 1x128 quantization of its BF16 rounding
+    (quantize) and float32 dweight [N] (want_dweight).
+    """
+    torch = _torch()
+    f32, b16 = types = _types()[1]
+    rows, n, ldd, dy_p = _rows_of(dy, "dy", types)
+    hr, hn, ldh, h_p = _rows_of(h, "h", types)
+    if (hr, hn) != (rows, n):
+        raise ValueError(f"h must be [{rows}, {n}], got [{hr}, {hn}]")
+    rstd_p, w_p = _vector(rstd, rows, (f32,), "rstd"), _vector(weight, n, types, "weight")
+    res_p, ldr = None, n
+    if dres is not None:
+        rr, rn, ldr, res_p = _rows_of(dres, "dres", types if out_dtype is None else (out_dtype,))
+        if (rr, rn) != (rows, n):
+            raise ValueError(f"dres must be [{rows}, {n}], got [{rr}, {rn}]")
+        out_dtype = dres.dtype
+    out_dtype = out_dtype or b16
+    if out_dtype not in types:
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    if not (want_dx or quantize or want_dweight):
+        raise ValueError("nothing to compute: ask for dx, quantize or dweight")
+    dev = _one_device(dy, h, rstd, weight, dres)
+    dx = _new(rows, n, out_dtype, dev) if want_dx else None
+    codes = scales = dw = work = None
+    ldc, need = n, 0
+    if quantize:
+        codes, ldc = _new_codes(rows, n, dev)
+        scales = _new(rows, (n + 127) // 128, f32, dev)
+    if want_dweight:
+        # one allocation: [dweight | workspace]
+        need = (_lib or load_library()).fp8q_rmsnorm_backward_workspace(rows, n)
+        pad = (n + 3) // 4 * 4
+        work = torch.empty_strided((pad + need // 4,), (1,), dtype=f32, device=dev)
+        dw = work.as_strided((n,), (1,))
+    at = _addr(dw)
+    _call(dev, "fp8q_rmsnorm_backward", dy_p, types.index(dy.dtype), rows, n, ldd, h_p, types.index(h.dtype), ldh, rstd_p, w_p,
+          types.index(weight.dtype), res_p, ldr, _addr(dx), types.index(out_dtype), n, _scale_mode(scale_mode), _addr(codes), ldc,
+          _addr(scales), at, at + 4 * pad if need else None, need)
+    return dx, codes, scales, dw
+
+
+def rmsnorm_quantize_t(h, rstd, weight, index=None, scale_mode="free"):
+    """The norm's output once more, from h, rstd and weight as for
+    ``rmsnorm_backward``, in 128x1 token-axis tiles: (codes [N, rows],
+    scales [N, ceil(rows/128)]), bit for bit ``quantize_act(y, "token_t")``
+    of the y that ``rmsnorm_quantize`` forms.
+
+    index: int32 [rows], the row of h behind every row of the token axis
+    (``moe_sort``'s token; outside h: zeros).  Default: every row of h.
+    """
+    types = _types()[1]
+    hr, n, ldh, h_p = _rows_of(h, "h", types)
+    rstd_p, w_p = _vector(rstd, hr, types[:1], "rstd"), _vector(weight, n, types, "weight")
+    rows, i_p = hr, None
+    if index is not None:
+        rows = index.numel() if isinstance(index, _types()[0]) else 0
+        i_p = _vector(index, rows, _types()[2:], "index")
+    dev = _one_device(h, rstd, weight, index)
+    codes, ldc = _new_codes(n, rows, dev)
+    scales = _new(n, (rows + 127) // 128, types[0], dev)
+    _call(dev, "fp8q_rmsnorm_quantize_t", h_p, types.index(h.dtype), hr, n, ldh, rstd_p, w_p, types.index(weight.dtype), i_p, rows,
+          _scale_mode(scale_mode), _addr(codes), ldc, _addr(scales))
+    return codes, scales
+
+
+def _score(score):
+    try:
+        return {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}[score]
+    except KeyError:
+        raise ValueError('score must be "softmax" or "sigmoid"') from None
+
+
+def moe_route(logits, topk, bias=None, score="sigmoid", groups=1, top_groups=1, group_score="top2", renormalize=True, scale=1.0,
+              index_dtype=None, want_scores=False, load=None):
+    """The router's choice: the topk experts of every token and their weights.
+
+    logits BF16 or float32 [tokens, E]; score "sigmoid" or "softmax".  The
+    choice goes by score + bias (float32 [E]), or by the logits without one,
+    within the top_groups best of `groups` groups of consecutive experts (by
+    their best expert, group_score "max", or their two best, "top2"); ties go
+    to the lower index.  Weights are scale * score, divided by their sum if
+    renormalize.  Experts whose logit or bias is -inf or NaN are never chosen;
+    what a token lacks is expert -1 with weight 0 (``moe_sort`` skips it).
+
+    Returns (experts int32 or index_dtype [tokens, topk], best first, weights
+    float32 [tokens, topk], scores float32 [tokens, E] with want_scores, else
+    None).  load: int32 [E], to which each expert's number of pairs is added.
+    """
+    torch = _torch()
+    tensor, types, i32 = _types()
+    tokens, n, ld, logits_p = _rows_of(logits, "logits", types)
+    bias_p = None if bias is None else _vector(bias, n, types[:1], "bias")
+    load_p = None if load is None else _vector(load, n, (i32,), "load")
+    index_dtype = index_dtype or i32
+    if index_dtype not in (i32, torch.int64):
+        raise TypeError("index_dtype must be torch.int32 or torch.int64")
+    # (topk and the groups go over as 64- and 32-bit integers)
+    if not 0 <= topk <= n or not 1 <= top_groups <= groups < 1 << 31:
+        raise ValueError("topk must be in 0 .. experts, top_groups in 1 .. groups")
+    if group_score not in ("max", "top2"):
+        raise ValueError('group_score must be "max" or "top2"')
+    dev = _one_device(logits, bias, load)
+    experts = _new(tokens, topk, index_dtype, dev)
+    weights = _new(tokens, topk, types[0], dev)
+    scores = _new(tokens, n, types[0], dev) if want_scores else None
+    _call(dev, "fp8q_moe_route", logits_p, types.index(logits.dtype), tokens, n, ld, bias_p, _score(score), groups, top_groups,
+          GROUP_MAX if group_score == "max" else GROUP_TOP_TWO, topk, bool(renormalize), scale,
+          INDEX_I32 if index_dtype == i32 else INDEX_I64, _addr(experts), _addr(weights), _addr(scores), load_p)
+    return experts, weights, scores
+
+
+def moe_route_backward(dweights, experts, logits, score="sigmoid", renormalize=True, scale=1.0, dscores=None, out_dtype=None):
+    """Gradient of ``moe_route``'s weights with respect to the logits, the
+    choice held fixed: dweights float32 and experts (int32 or int64) [tokens,
+    topk], logits, score, renormalize and scale as there.  dscores: float32
+    [tokens, E], added as the gradient of the scores.  Returns dlogits
+    [tokens, E], out_dtype or the logits' type.
+    """
+    torch = _torch()
+    tensor, types, i32 = _types()
+    tokens, n, ld, logits_p = _rows_of(logits, "logits", types)
+    _contig_f32(dweights, "dweights")
+    if not isinstance(experts, tensor) or experts.dtype not in (i32, torch.int64):
+        raise TypeError("experts must be an int32 or int64 torch.Tensor")
+    shape = tuple(dweights.shape)
+    if len(shape) != 2 or shape[0] != tokens or tuple(experts.shape) != shape or not experts.is_contiguous():
+        raise ValueError(f"dweights and experts must be contiguous [{tokens}, topk] tensors")
+    if shape[1] > n:
+        raise ValueError("more choices than experts")
+    if dscores is not None:
+        _contig_f32(dscores, "dscores")
+        if tuple(dscores.shape) != (tokens, n):
+            raise ValueError(f"dscores must be [{tokens}, {n}], got {tuple(dscores.shape)}")
+    out_dtype = out_dtype or logits.dtype
+    if out_dtype not in types:
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    dev = _one_device(logits, dweights, experts, dscores)
+    dlogits = _new(tokens, n, out_dtype, dev)
+    _call(dev, "fp8q_moe_route_backward", _addr(dweights), _addr(experts), INDEX_I32 if experts.dtype == i32 else INDEX_I64, tokens,
+          shape[1], logits_p, types.index(logits.dtype), n, ld, _score(score), bool(renormalize), scale, _addr(dscores), _addr(dlogits),
+          types.index(out_dtype), n)
+    return dlogits

@@ -151,4 +151,100 @@ hipError_t launch_grouped_wgrad(const uint8_t* dy_t, const float* dy_scales, con
                                 const float* x_scales, const int32_t* offsets, int groups, int cap, int nout,
                                 int kin, int acc, float* dw, int64_t lddw, hipStream_t stream);
 
+// RMS norm (norm.hip): res == nullptr: h = x (h, ldh unused).  h, y, codes,
+// rstd == nullptr: not written.
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* res;
+  int64_t ldr;
+  void* h;
+  int64_t ldh;
+  const void* weight;
+  uint16_t* y;
+  int64_t ldy;
+  uint8_t* codes;
+  int64_t ldc;
+  float* scales;
+  float* rstd;
+  double eps;
+  int rows, n;
+  bool xf32, sf32, wf32, pow2;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+// dres == nullptr: no such term; dx, codes, dweight == nullptr: not written.
+// partial: float [norm_dw_blocks(rows), n], only used for dweight.
+struct NormBwdArgs {
+  const void* dy;
+  int64_t lddy;
+  const void* h;
+  int64_t ldh;
+  const float* rstd;
+  const void* weight;
+  const void* dres;
+  int64_t lddr;
+  void* dx;
+  int64_t lddx;
+  uint8_t* codes;
+  int64_t ldc;
+  float* scales;
+  float* dweight;
+  float* partial;
+  int rows, n;
+  bool df32, hf32, wf32, of32, pow2;
+};
+// blocks of rows whose shares of the gain's gradient are summed apart
+inline int norm_dw_blocks(int rows) {
+  const int64_t want = ((int64_t)rows + 31) / 32;
+  return (int)(want < 256 ? want : 256);
+}
+hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t stream);
+// index == nullptr: row t of the output is row t of h
+struct NormTokenArgs {
+  const void* h;
+  int64_t ldh;
+  const float* rstd;
+  const void* weight;
+  const int* index;
+  uint8_t* codes;
+  int64_t ldc;
+  float* scales;
+  int rows, src_rows, n;
+  bool hf32, wf32, pow2;
+};
+hipError_t launch_norm_token(const NormTokenArgs& a, hipStream_t stream);
+
+// The router's choice (moe_gate.hip).
+constexpr int kMaxGateExperts = 512;
+constexpr int kMaxGateChoices = 64;  // one lane each
+constexpr int kMaxGateGroups = 64;
+constexpr int kMaxGateGrid = 1 << 20;
+struct GateArgs {
+  const void* logits;
+  int64_t ld;
+  const float* bias;  // null: none
+  void* chosen;
+  float* weights;
+  float* scores;  // null: not written
+  int* load;      // null: not counted
+  double scale;
+  int tokens, experts, topk, groups, top_groups;
+  int group_lanes;  // (set by the launcher)
+  bool lf32, i64, sigmoid, two_best, renormalize;
+};
+hipError_t launch_gate(GateArgs a, hipStream_t stream);
+struct GateBwdArgs {
+  const float* dweights;
+  const void* chosen;
+  const void* logits;
+  int64_t ld;
+  const float* dscores;  // null: none
+  void* dlogits;
+  int64_t ldd;
+  double scale;
+  int tokens, experts, topk;
+  bool lf32, of32, i64, sigmoid, renormalize;
+};
+hipError_t launch_gate_backward(const GateBwdArgs& a, hipStream_t stream);
+
 }  // namespace fp8q

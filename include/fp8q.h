@@ -109,6 +109,8 @@ enum { FP8Q_OUT_F32 = 0, FP8Q_OUT_BF16 = 1 };
  *    that are not powers of two give wrong results. */
 enum { FP8Q_ACC_FP32 = 0, FP8Q_ACC_FP8_MFMA = 1, FP8Q_ACC_FP8_MFMA_SCALED = 2, FP8Q_ACC_FP32_POW2 = 3 };
 enum { FP8Q_INDEX_I32 = 0, FP8Q_INDEX_I64 = 1 };
+enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 };
+enum { FP8Q_GROUP_MAX = 0, FP8Q_GROUP_TOP_TWO = 1 };
 enum {
   FP8Q_TILE_ROW = 0,    /* 1x128 tiles along cols: codes [rows, ld_codes], scales [rows, ceil(cols/128)] */
   FP8Q_TILE_TOKEN_T = 1 /* 128x1 tiles along rows (the token axis), codes written transposed:
@@ -456,6 +458,133 @@ fp8q_status fp8q_grouped_wgrad_ex(const uint8_t* dy_t, const float* dy_scales,
                                   const uint8_t* x_t, const float* x_scales,
                                   const int32_t* offsets, int32_t G, int64_t rows_cap,
                                   int64_t Nout, int64_t Kin, int acc, float* dw, int64_t ld_dw, hipStream_t stream);
+
+/* ---- between a block's linear layers ----------------------------------------
+ * Forward: fp8q_rmsnorm_quantize (its codes go to fp8q_gemm, or through
+ * fp8q_gather_rows to the experts), the router's logits, fp8q_moe_route,
+ * fp8q_moe_sort.  Backward: fp8q_moe_route_backward (from the dweights of
+ * fp8q_moe_combine_backward), fp8q_rmsnorm_quantize_t (the operand of
+ * fp8q_wgrad, or with fp8q_moe_sort's token list of fp8q_grouped_wgrad) and
+ * fp8q_rmsnorm_backward. */
+
+/* Residual addition, RMS norm and the quantization of its output, from one
+ * read of the row (jp-study.kr doc 258368 ¶1: activations are quantized
+ * online; tmdrlife.com wr_id=13334 ¶1: without a trip of the BF16 tensor
+ * through HBM).  Per row, rn being the rounding to the stream's type and
+ * rn32 / fl the one to float32:
+ *   h = rn(x + residual)                       (h = x without a residual)
+ *   rstd = rn32(1 / sqrt(sum h^2 / N + eps))   (the sum in 64 bits)
+ *   y[n] = bf16_rne(fl(fl(h[n] * rstd) * weight[n]))
+ * x [rows, ld_x >= N] is FP8Q_OUT_F32 or FP8Q_OUT_BF16 (x_dtype), residual
+ * [rows, ld_residual >= N] and h [rows, ld_h >= N] are stream_dtype, weight
+ * [N] is weight_dtype.  residual may be NULL (then h must be, too).  Each of
+ * h, y_bf16 [rows, ld_y >= N], codes and rstd (float32 [rows]) is written
+ * where its pointer is not NULL; one at least must be given.  codes [rows,
+ * ld_codes >= N] and scales [rows, ceil(N/128)] are bit for bit what
+ * fp8q_quantize_act(FP8Q_TILE_ROW, scale_mode) writes for that y.  The
+ * outputs of a row do not depend on the other rows nor on their number.  h
+ * may be residual itself with the same stride (the stream is then updated in
+ * place).  eps > 0 and finite.  Infinities and NaN follow float32 arithmetic
+ * in h, rstd and y of their row; for the codes every y must be finite.  rstd
+ * keeps its precision while it is a normal float32 number (a root of the mean
+ * square below 2^126).  With N = 0 rstd is rn32(1 / sqrt(eps)).  N < 2^30,
+ * else FP8Q_ERR_SHAPE. */
+fp8q_status fp8q_rmsnorm_quantize(const void* x, int x_dtype, int64_t rows, int64_t N, int64_t ld_x,
+                                  const void* residual, int stream_dtype, int64_t ld_residual, void* h, int64_t ld_h,
+                                  const void* weight, int weight_dtype, double eps, void* y_bf16, int64_t ld_y,
+                                  int scale_mode, uint8_t* codes, int64_t ld_codes, float* scales, float* rstd,
+                                  hipStream_t stream);
+
+/* Gradient of the norm for dy [rows, ld_dy >= N] (dy_dtype), from the h and
+ * rstd of the forward pass.  With g = fl(dy * weight), t = fl(h * rstd) and
+ * c = rn32(sum(g * h) * rstd / N), the sum in 64 bits:
+ *   dx = fl(fl(fl(g - fl(t * c)) * rstd) + dresidual)
+ *   dweight[n] = sum over rows of dy * t       (float32)
+ * dx is the gradient of x and of the residual alike; dresidual, the gradient
+ * that reaches h past the norm, has dx's type and may be NULL.  dx [rows,
+ * ld_dx >= N] (dx_dtype, rounded once), the 1x128 quantization of its BF16
+ * rounding (dx_codes [rows, ld_codes >= N], dx_scales [rows, ceil(N/128)],
+ * scale_mode) and dweight [N] are each written where the pointer is not NULL;
+ * one at least must be given.  dx may be dresidual itself with the same
+ * stride.  Without rows dweight is zero.  dweight is summed in an order that
+ * depends on the sizes alone.  workspace: DEVICE memory of at least
+ * fp8q_rmsnorm_backward_workspace(rows, N) bytes for dweight (without it 0:
+ * it may be NULL), used until the call's work is done; calls that may run at
+ * the same time need one each.  A missing or small workspace gives
+ * FP8Q_ERR_INVALID_ARG.  Infinities and NaN follow float32 arithmetic in dx
+ * and dweight; for the codes every dx must be a finite BF16 value.
+ * N < 2^30, else FP8Q_ERR_SHAPE. */
+int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t N);
+fp8q_status fp8q_rmsnorm_backward(const void* dy, int dy_dtype, int64_t rows, int64_t N, int64_t ld_dy,
+                                  const void* h, int h_dtype, int64_t ld_h, const float* rstd,
+                                  const void* weight, int weight_dtype, const void* dresidual, int64_t ld_dresidual,
+                                  void* dx, int dx_dtype, int64_t ld_dx, int scale_mode, uint8_t* dx_codes,
+                                  int64_t ld_codes, float* dx_scales, float* dweight, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t stream);
+
+/* The norm's output formed again from h and rstd, in the token-axis tiles of
+ * a weight gradient (tmdrlife.com wr_id=13334 ¶4: outputs are recomputed in
+ * the backward pass; jp-study.kr doc 258368 ¶3: Wgrad runs in FP8):
+ *   row t of the token axis = y of row index[t]   (row t with index NULL)
+ * with y as fp8q_rmsnorm_quantize forms it, bit for bit, and codes_t [N,
+ * ld_codes_t >= rows], scales_t [N, ceil(rows/128)] bit for bit what
+ * fp8q_quantize_act(FP8Q_TILE_TOKEN_T, scale_mode) writes for that BF16
+ * tensor [rows, N].  h [h_rows, ld_h >= N] (h_dtype), rstd float32 [h_rows].
+ * index: DEVICE int32[rows] (the token list of fp8q_moe_sort); a row whose
+ * index lies outside [0, h_rows) is zero.  Without it rows must be h_rows.
+ * Every y must be finite.  Fewer than 2^24 workgroups of 128 rows x 64
+ * columns, else FP8Q_ERR_SHAPE. */
+fp8q_status fp8q_rmsnorm_quantize_t(const void* h, int h_dtype, int64_t h_rows, int64_t N, int64_t ld_h,
+                                    const float* rstd, const void* weight, int weight_dtype, const int32_t* index,
+                                    int64_t rows, int scale_mode, uint8_t* codes_t, int64_t ld_codes_t,
+                                    float* scales_t, hipStream_t stream);
+
+/* The router's choice of experts (jp-study.kr doc 258368 ¶2: 256 routed
+ * experts, eight per token) from logits x [tokens, ld_logits >= E]
+ * (logits_dtype).  Scores s, in 64 bits:
+ *   FP8Q_SCORE_SIGMOID  s = 1 / (1 + exp(-x))
+ *   FP8Q_SCORE_SOFTMAX  s = exp(x) / sum over the row of exp(x)
+ * The choice goes by s + bias (bias float32 [E], for balance; it does not
+ * enter the weights), or with bias NULL by x, with which the scores rise.
+ * With groups > 1 the experts are groups of E / groups consecutive ones and
+ * only those of the top_groups best groups are open: a group ranks by its best
+ * expert (FP8Q_GROUP_MAX) or by the sum of its two best (FP8Q_GROUP_TOP_TWO;
+ * of their scores with bias NULL).  Equal groups and experts go by the lower
+ * index.  Written per token, best first:
+ *   experts[t, j]  the j-th best open expert, int32 or int64 (index_dtype)
+ *   weights[t, j]  scale * s, or with renormalize scale * s / (sum of s over
+ *                  the token's chosen experts), rounded to float32; 0 where
+ *                  that sum is 0
+ *   scores[t, e]   float32 [tokens, E], where the pointer is not NULL
+ *   load[e]        int32 [E], where the pointer is not NULL: the number of
+ *                  pairs that chose e is added to it
+ * +inf counts as the largest finite logit.  An expert whose logit is -inf or
+ * NaN, or whose bias is, is never chosen (a logit of -inf or NaN has score 0);
+ * where a token has fewer than topk others, the rest of its row is expert -1
+ * with weight 0, which fp8q_moe_sort gives no row.  A token whose logits are
+ * all -inf (padding) has no experts.
+ * E <= 512, groups <= 64 and a divisor of E, topk <= 64 and at most the open
+ * experts' number, else FP8Q_ERR_SHAPE. */
+fp8q_status fp8q_moe_route(const void* logits, int logits_dtype, int64_t tokens, int64_t E, int64_t ld_logits,
+                           const float* bias, int score, int32_t groups, int32_t top_groups, int group_score,
+                           int64_t topk, int renormalize, double scale, int index_dtype, void* experts,
+                           float* weights, float* scores, int32_t* load, hipStream_t stream);
+
+/* Gradient of fp8q_moe_route's weights (and scores) with respect to the
+ * logits, the choice held fixed:
+ *   ds[e] = sum over j with experts[t, j] = e of scale * dweights[t, j], or with
+ *           renormalize of scale * (dweights[t, j] - sum_k dweights[t, k] w_k) / S
+ *           (S the sum of the chosen scores, w_k = s_k / S; 0 where S is 0)
+ *   plus dscores[t, e] (float32 [tokens, E]; may be NULL)
+ *   sigmoid: dlogits = ds * s * (1 - s),  softmax: dlogits = s * (ds - sum_e ds * s)
+ * over E logits as for fp8q_moe_route, with its score, renormalize and scale.
+ * An expert outside [0, E) adds nothing (its dweights is not used).  dlogits
+ * [tokens, ld_dlogits >= E] (dlogits_dtype) is written whole; it is 0 where
+ * the logit is -inf or NaN.  Sizes as for fp8q_moe_route. */
+fp8q_status fp8q_moe_route_backward(const float* dweights, const void* experts, int index_dtype, int64_t tokens,
+                                    int64_t topk, const void* logits, int logits_dtype, int64_t E, int64_t ld_logits,
+                                    int score, int renormalize, double scale, const float* dscores, void* dlogits,
+                                    int dlogits_dtype, int64_t ld_dlogits, hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* fp8q_status_string(fp8q_status s);
