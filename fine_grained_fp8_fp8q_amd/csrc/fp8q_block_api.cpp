@@ -45,15 +45,15 @@ fp8q_status fp8q_rmsnorm_quantize(const void* x, int x_dtype, int64_t rows, int6
   fp8q::NormArgs a{};
   a.x = x; a.ldx = ld_x; a.res = residual; a.ldr = ld_residual; a.h = h; a.ldh = ld_h; a.weight = weight;
   a.y = static_cast<uint16_t*>(y_bf16); a.ldy = ld_y; a.codes = codes; a.ldc = ld_codes; a.scales = scales; a.rstd = rstd;
-  a.eps = eps; a.rows = (int)rows; a.n = (int)N;
+  a.eps = eps; a.inv_n = N > 0 ? 1.0 / (double)N : 0.0; a.rows = (int)rows; a.n = (int)N;
   a.xf32 = x_dtype == FP8Q_OUT_F32; a.sf32 = stream_dtype == FP8Q_OUT_F32; a.wf32 = weight_dtype == FP8Q_OUT_F32;
   a.pow2 = scale_mode == FP8Q_SCALE_POW2;
   return launched(fp8q::launch_norm(a, stream));
 }
 
 int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t N) {
-  if (!dim_ok(rows) || !dim_ok(N) || N >= kMaxRow) return 0;
-  return (int64_t)fp8q::norm_dw_blocks((int)rows) * N * (int64_t)sizeof(float);
+  if (!dim_ok(rows) || !dim_ok(N) || N >= kMaxRow || rows == 0 || N == 0) return 0;
+  return fp8q::norm_bwd_shape((int)rows, (int)N).blocks * fp8q::norm_partial_ld((int)N) * (int64_t)sizeof(float);
 }
 
 fp8q_status fp8q_rmsnorm_backward(const void* dy, int dy_dtype, int64_t rows, int64_t N, int64_t ld_dy, const void* h, int h_dtype,
@@ -80,7 +80,7 @@ fp8q_status fp8q_rmsnorm_backward(const void* dy, int dy_dtype, int64_t rows, in
   fp8q::NormBwdArgs a{};
   a.dy = dy; a.lddy = ld_dy; a.h = h; a.ldh = ld_h; a.rstd = rstd; a.weight = weight; a.dres = dresidual; a.lddr = ld_dresidual;
   a.dx = dx; a.lddx = ld_dx; a.codes = dx_codes; a.ldc = ld_codes; a.scales = dx_scales; a.dweight = dweight;
-  a.partial = static_cast<float*>(workspace); a.rows = (int)rows; a.n = (int)N;
+  a.partial = static_cast<float*>(workspace); a.inv_n = 1.0 / (double)N; a.rows = (int)rows; a.n = (int)N;
   a.df32 = dy_dtype == FP8Q_OUT_F32; a.hf32 = h_dtype == FP8Q_OUT_F32; a.wf32 = weight_dtype == FP8Q_OUT_F32;
   a.of32 = dx_dtype == FP8Q_OUT_F32; a.pow2 = scale_mode == FP8Q_SCALE_POW2;
   return launched(fp8q::launch_norm_backward(a, stream));

@@ -167,13 +167,27 @@ struct NormArgs {
   int64_t ldc;
   float* scales;
   float* rstd;
-  double eps;
+  double eps, inv_n;  // inv_n: 1 / n, or 0
   int rows, n;
   bool xf32, sf32, wf32, pow2;
 };
+// A row of up to kMaxNormRow columns stays in the registers of its workgroup:
+// chunks of eight columns that a thread of the forward pass keeps, and the
+// threads (0: the row is longer and is read twice).
+constexpr int kMaxNormRow = 16384;
+inline int norm_chunks(int rows, int n) {
+  const int items = (n + 7) / 8;
+  return items <= 256 ? 1 : items > 512 && rows >= 4096 ? 4 : 2;
+}
+inline int norm_threads(int n, int chunks) {
+  if (n > kMaxNormRow) return 0;
+  const int per = ((n + 7) / 8 + chunks - 1) / chunks;
+  return per == 0 ? 64 : (per + 63) / 64 * 64;
+}
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 // dres == nullptr: no such term; dx, codes, dweight == nullptr: not written.
-// partial: float [norm_dw_blocks(rows), n], only used for dweight.
+// partial: float [norm_bwd_shape(rows, n).blocks, norm_partial_ld(n)], only
+// used for dweight.
 struct NormBwdArgs {
   const void* dy;
   int64_t lddy;
@@ -190,14 +204,31 @@ struct NormBwdArgs {
   float* scales;
   float* dweight;
   float* partial;
+  int64_t ldp;  // (set by the launcher)
+  double inv_n;  // 1 / n
   int rows, n;
   bool df32, hf32, wf32, of32, pow2;
 };
-// blocks of rows whose shares of the gain's gradient are summed apart
-inline int norm_dw_blocks(int rows) {
-  const int64_t want = ((int64_t)rows + 31) / 32;
-  return (int)(want < 256 ? want : 256);
+// How the backward pass goes over its rows (rows, n > 0): a wave a row up to
+// 1024 columns, a workgroup above, `chunks` of eight columns a thread (0: the
+// row is longer than kMaxNormRow), `blocks` workgroups (of longer rows: blocks
+// of them), each with a share of the gain's gradient.
+struct NormBwdShape {
+  int threads, chunks, blocks;
+  bool wave;
+};
+constexpr int kNormBwdBlocks = 768;
+inline NormBwdShape norm_bwd_shape(int rows, int n) {
+  const int items = (n + 7) / 8;
+  NormBwdShape s{};
+  s.wave = items <= 128;
+  s.chunks = n > kMaxNormRow ? 0 : items <= 64 ? 1 : 2;
+  s.threads = s.wave ? 256 : s.chunks ? ((items + 1) / 2 + 63) / 64 * 64 : 1024;
+  const int64_t want = s.wave ? ((int64_t)rows + 3) / 4 : s.chunks ? rows : ((int64_t)rows + 31) / 32;
+  s.blocks = (int)(want < kNormBwdBlocks ? want : kNormBwdBlocks);
+  return s;
 }
+inline int64_t norm_partial_ld(int n) { return ((int64_t)n + 7) / 8 * 8; }
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t stream);
 // index == nullptr: row t of the output is row t of h
 struct NormTokenArgs {

@@ -24,27 +24,6 @@ namespace fp8q {
 // instead of four (the free scale is a corrected quotient and a corrected
 // reciprocal, about 10 instructions).
 
-// Tile u's scale state, from lane u of each DPP row.
-template <bool POW2, int U>
-__device__ __forceinline__ TileScale row_tile_scale(const TileScale& tm) {
-  TileScale ts;
-  ts.s = 0.0f;  // (stored by lane u itself)
-  if constexpr (POW2) {
-    ts.div = 1.0f;
-    ts.mul = 1.0f;
-    ts.xscale = 1.0f;
-    ts.slow = false;
-    ts.neg_e = (int)row_bcast<U>((uint32_t)tm.neg_e);
-  } else {
-    ts.div = row_bcast<U>(tm.div);
-    ts.mul = row_bcast<U>(tm.mul);
-    ts.neg_e = 0;
-    ts.slow = row_bcast<U>((uint32_t)tm.slow) != 0u;
-    ts.xscale = ts.slow ? 0x1p64f : 1.0f;
-  }
-  return ts;
-}
-
 template <bool POW2>
 __device__ __forceinline__ void quant_rows_body(int bid, int nblocks, const uint16_t* __restrict__ x, int cols,
                                                 int64_t ldx, uint8_t* __restrict__ codes, int64_t ldc,

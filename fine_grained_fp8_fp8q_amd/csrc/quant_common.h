@@ -253,6 +253,27 @@ __device__ __forceinline__ float row_bcast(float v) {
   return __uint_as_float(row_bcast<N>(__float_as_uint(v)));
 }
 
+// Tile u's scale state, from lane u of each DPP row.
+template <bool POW2, int U>
+__device__ __forceinline__ TileScale row_tile_scale(const TileScale& tm) {
+  TileScale ts;
+  ts.s = 0.0f;  // (stored by lane u itself)
+  if constexpr (POW2) {
+    ts.div = 1.0f;
+    ts.mul = 1.0f;
+    ts.xscale = 1.0f;
+    ts.slow = false;
+    ts.neg_e = (int)row_bcast<U>((uint32_t)tm.neg_e);
+  } else {
+    ts.div = row_bcast<U>(tm.div);
+    ts.mul = row_bcast<U>(tm.mul);
+    ts.neg_e = 0;
+    ts.slow = row_bcast<U>((uint32_t)tm.slow) != 0u;
+    ts.xscale = ts.slow ? 0x1p64f : 1.0f;
+  }
+  return ts;
+}
+
 // Loads up to 8 BF16 values (nvalid may be <= 0 or >= 8); missing ones are +0.
 __device__ __forceinline__ uint4 load8_masked(const uint16_t* p, int nvalid) {
   uint32_t w[4];

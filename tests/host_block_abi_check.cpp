@@ -73,9 +73,16 @@ int main() {
 
   // backward: the workspace is what the launch will write, for every size that is accepted
   for (int64_t rows : {int64_t(0), int64_t(1), int64_t(31), int64_t(33), int64_t(5000), big})
-    for (int64_t n : {int64_t(1), int64_t(7), int64_t(7168), row - 1}) {
+    for (int64_t n : {int64_t(1), int64_t(7), int64_t(512), int64_t(513), int64_t(1024), int64_t(2048), int64_t(2049), int64_t(7168), int64_t(16384),
+                      int64_t(16385), int64_t(32768), int64_t(32769), row - 1}) {
       const int64_t need = fp8q_rmsnorm_backward_workspace(rows, n);
-      CHECK(need >= 0 && need % 4 == 0 && need >= (int64_t)fp8q::norm_dw_blocks((int)rows) * n * 4);
+      CHECK(need % 16 == 0 && (need > 0) == (rows > 0));
+      if (rows > 0) {
+        const fp8q::NormBwdShape s = fp8q::norm_bwd_shape((int)rows, (int)n);
+        CHECK(need == s.blocks * fp8q::norm_partial_ld((int)n) * 4 && s.blocks >= 1 && s.blocks <= rows && fp8q::norm_partial_ld((int)n) >= n);
+        CHECK(s.threads >= 64 && s.threads <= 1024 && s.threads % 64 == 0);
+        CHECK(s.chunks == 0 ? n > 16384 : (int64_t)(s.wave ? 64 : s.threads) * s.chunks * 8 >= n);  // a row fits
+      }
       if (need > 0) {
         CHECK(fp8q_rmsnorm_backward(P, 1, rows, n, n, P, 1, n, F, P, 1, nullptr, 0, P, 1, n, 0, nullptr, 0, nullptr, F, P, need - 1, nullptr) == FP8Q_ERR_INVALID_ARG);
         CHECK(fp8q_rmsnorm_backward(P, 1, rows, n, n, P, 1, n, F, P, 1, nullptr, 0, P, 1, n, 0, nullptr, 0, nullptr, F, nullptr, need, nullptr) == FP8Q_ERR_INVALID_ARG);
@@ -89,6 +96,14 @@ int main() {
   CHECK(g_bwd.dy == P && g_bwd.lddy == 65 && g_bwd.h == R && g_bwd.ldh == 66 && g_bwd.weight == R && g_bwd.dres == R && g_bwd.lddr == 67 && g_bwd.lddx == 68 &&
         g_bwd.ldc == 69 && g_bwd.df32 && !g_bwd.hf32 && g_bwd.wf32 && !g_bwd.of32 && g_bwd.pow2);
   CHECK(fp8q_rmsnorm_backward(P, 0, 1, row, row, R, 1, row, F, R, 0, nullptr, 0, P, 1, row, 0, nullptr, 0, nullptr, nullptr, nullptr, 0, nullptr) == FP8Q_ERR_SHAPE);
+
+  // the forward pass: every width is held by the threads, or goes to the kernel of long rows
+  for (int rows : {1, 4095, 4096, (int)big})
+    for (int n : {0, 1, 512, 2048, 2049, 4096, 4097, 7168, 16384, 16385, 32768, 32769, (int)row - 1}) {
+      const int chunks = fp8q::norm_chunks(rows, n), threads = fp8q::norm_threads(n, chunks);
+      CHECK((chunks == 1 || chunks == 2 || chunks == 4) && threads % 64 == 0 && threads <= (chunks == 4 ? 512 : 1024));
+      CHECK(threads ? (int64_t)threads * chunks * 8 >= n : n > 16384);
+    }
 
   // token tiles: the number of workgroups neither overflows nor passes
   CHECK(fp8q_rmsnorm_quantize_t(P, 0, 10, 64, 65, F, P, 1, I, 300, 1, U, 304, F, nullptr) == FP8Q_OK);
