@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libfp8q.so")
 STREAMREF_LIB = os.path.join(PKG, "libfp8q_streamref.so")
 
 SOURCES = ["quant.hip", "gemm.hip", "gemm_small.hip", "moe.hip", "moe_route.hip", "moe_swiglu_bwd.hip", "wgrad_grouped.hip", "norm.hip",
-           "norm_token.hip", "moe_gate.hip", "fp8q_api.cpp",
+           "norm_bwd.hip", "norm_token.hip", "moe_gate.hip", "fp8q_api.cpp",
            "fp8q_moe_api.cpp", "fp8q_block_api.cpp"]
 
 # -ffp-contract=off: every fused multiply-add in the kernels is written out

@@ -186,8 +186,8 @@ inline int norm_threads(int n, int chunks) {
 }
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 // dres == nullptr: no such term; dx, codes, dweight == nullptr: not written.
-// partial: float [norm_bwd_shape(rows, n).blocks, norm_partial_ld(n)], only
-// used for dweight.
+// partial: float [norm_bwd_blocks(rows), norm_partial_ld(n)], only used for
+// dweight.
 struct NormBwdArgs {
   const void* dy;
   int64_t lddy;
@@ -209,25 +209,33 @@ struct NormBwdArgs {
   int rows, n;
   bool df32, hf32, wf32, of32, pow2;
 };
-// How the backward pass goes over its rows (rows, n > 0): a wave a row up to
-// 1024 columns, a workgroup above, `chunks` of eight columns a thread (0: the
-// row is longer than kMaxNormRow), `blocks` workgroups (of longer rows: blocks
-// of them), each with a share of the gain's gradient.
+// How the backward pass goes over its rows (rows, n > 0; f32: some tensor of
+// them is float32): a wave a row while `chunks` of eight columns a thread hold
+// it (0: the row is longer than that of 512 threads), a workgroup above;
+// `blocks` workgroups (of longer rows: blocks of them), each with a share of
+// the gain's gradient.  As few blocks as keep the memory busy, since every
+// share is written and read again: 8192 rows of 7168 BF16 columns take 86 us
+// with 256 blocks, 90 with 512 (as many as fit), 94 with 1024; 4096 of 4096
+// 34.9, 33.4 and 37.1; 32768 of 512 34.5, 29.0 and 31.1.
 struct NormBwdShape {
   int threads, chunks, blocks;
   bool wave;
 };
-constexpr int kNormBwdBlocks = 768;
-inline NormBwdShape norm_bwd_shape(int rows, int n) {
-  const int items = (n + 7) / 8;
+constexpr int kMaxNormGrid = 1 << 20;  // workgroups; more rows go round
+constexpr int kNormBwdBlocks = 512;
+inline NormBwdShape norm_bwd_shape(int rows, int n, bool f32) {
+  const int items = (n + 7) / 8, most = f32 ? 2 : 4;
   NormBwdShape s{};
-  s.wave = items <= 128;
-  s.chunks = n > kMaxNormRow ? 0 : items <= 64 ? 1 : 2;
-  s.threads = s.wave ? 256 : s.chunks ? ((items + 1) / 2 + 63) / 64 * 64 : 1024;
+  s.wave = items <= 64 * most;
+  s.chunks = n > kMaxNormRow / (f32 ? 2 : 1) ? 0 : items <= 64 ? 1 : items <= 128 ? 2 : most;
+  s.threads = s.wave ? 256 : s.chunks ? ((items + most - 1) / most + 63) / 64 * 64 : 1024;
   const int64_t want = s.wave ? ((int64_t)rows + 3) / 4 : s.chunks ? rows : ((int64_t)rows + 31) / 32;
-  s.blocks = (int)(want < kNormBwdBlocks ? want : kNormBwdBlocks);
+  const int most_blocks = (s.wave ? s.chunks < 4 : s.threads < 256) || !s.chunks ? kNormBwdBlocks : kNormBwdBlocks / 2;
+  s.blocks = (int)(want < most_blocks ? want : most_blocks);
   return s;
 }
+// blocks of the workspace: no shape has more
+inline int norm_bwd_blocks(int rows) { return rows < kNormBwdBlocks ? rows : kNormBwdBlocks; }
 inline int64_t norm_partial_ld(int n) { return ((int64_t)n + 7) / 8 * 8; }
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t stream);
 // index == nullptr: row t of the output is row t of h

@@ -14,10 +14,9 @@
 
 namespace fp8q {
 
-// Eight columns of a row of n, as they come; those past its end are +0.  A
-// row's last chunk is read as its last eight columns and moved down, so that
-// it costs no load after another (column by column a row of 1030 took twice
-// the time of one of 1024).
+// The last s of eight values that a chunk at a row's end was loaded too early:
+// a row's last chunk is read as its last eight columns and moved down once it
+// is used, so that it costs no branch and no load after another.
 __device__ __forceinline__ Raw<false, 8> moved_down(Raw<false, 8> r, int s) {
   if (s & 4) r = Raw<false, 8>{{r.w[2], r.w[3], 0, 0}};
   if (s & 2) r = Raw<false, 8>{{r.w[1], r.w[2], r.w[3], 0}};
@@ -33,16 +32,101 @@ __device__ __forceinline__ Raw<true, 8> moved_down(Raw<true, 8> r, int s) {
   if (s & 1) r = Raw<true, 8>{{r.w[1], r.w[2], r.w[3], r.w[4], r.w[5], r.w[6], r.w[7], 0}};
   return r;
 }
-template <bool F32, bool VEC, bool KEEP>
-__device__ __forceinline__ Raw<F32, 8> ld_row8(const void* base, int64_t row_at, int col, int n) {
-  if constexpr (VEC) {
-    return ld_raw<F32, 8, KEEP>(base, row_at + col, 8, true);
-  } else {
-    if (n < 8) return ld_raw<F32, 8, true>(base, row_at + col, n - col, false);
-    const Raw<F32, 8> r = ld_raw<F32, 8, true>(base, row_at + min(col, n - 8), 8, false);
-    return n - col < 8 ? moved_down(r, 8 - (n - col)) : r;
+
+// The first `left` (1 .. 7) of eight values in three stores at most.
+__device__ __forceinline__ void st_part(uint16_t* p, Raw<false, 8> r, int left) {
+  if (left & 4) {
+    *reinterpret_cast<Any8*>(p) = Any8{{r.w[0], r.w[1]}};
+    r = Raw<false, 8>{{r.w[2], r.w[3], 0, 0}};
+    p += 4;
   }
+  if (left & 2) {
+    p[0] = (uint16_t)r.w[0];
+    p[1] = (uint16_t)(r.w[0] >> 16);
+    r.w[0] = r.w[1];
+    p += 2;
+  }
+  if (left & 1) p[0] = (uint16_t)r.w[0];
 }
+__device__ __forceinline__ void st_part(float* p, Raw<true, 8> r, int left) {
+  uint32_t* q = reinterpret_cast<uint32_t*>(p);
+  if (left & 4) {
+    *reinterpret_cast<Any16*>(q) = Any16{{r.w[0], r.w[1], r.w[2], r.w[3]}};
+    r = Raw<true, 8>{{r.w[4], r.w[5], r.w[6], 0, 0, 0, 0, 0}};
+    q += 4;
+  }
+  if (left & 2) {
+    q[0] = r.w[0];
+    q[1] = r.w[1];
+    r.w[0] = r.w[2];
+    q += 2;
+  }
+  if (left & 1) q[0] = r.w[0];
+}
+
+// One row of a tensor.  Aligned rows (VEC: 16-byte boundaries, whole chunks)
+// go through a buffer resource of the row's bytes: past its end loads give 0
+// and stores do nothing, without a branch, and a chunk of every row has the
+// same offset.  Others are loaded by unaligned vector loads (see moved_down) and
+// settled before use.  A row that is not `on` has no bytes, or if not VEC is
+// one that may be read; KEEP: plain loads instead of streaming ones.
+template <bool F32, bool VEC, bool KEEP = true>
+struct Row {
+  static constexpr int kBytes = F32 ? 4 : 2;
+  __amdgpu_buffer_rsrc_t buf;
+  uint8_t* base;
+  int n;
+  __device__ __forceinline__ Row(const void* p, int64_t at, int columns, bool on = true) {
+    base = static_cast<uint8_t*>(const_cast<void*>(p)) + at * kBytes;
+    n = columns;
+    if constexpr (VEC) buf = __builtin_amdgcn_make_buffer_rsrc(base, 0, on ? n * kBytes : 0, 0x00020000);
+  }
+  __device__ __forceinline__ Raw<F32, 8> load(int col) const {
+    Raw<F32, 8> r;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < Raw<F32, 8>::N; i += 4) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(buf, col * kBytes + 4 * i, 0, KEEP ? 0 : 2);
+        r.w[i] = v[0];
+        r.w[i + 1] = v[1];
+        r.w[i + 2] = v[2];
+        r.w[i + 3] = v[3];
+      }
+      return r;
+    } else {
+      if (n < 8) return ld_raw<F32, 8, true>(base, 0, col == 0 ? n : 0, false);
+      return ld_raw<F32, 8, true>(base, min(col, n - 8), 8, false);
+    }
+  }
+  __device__ __forceinline__ void settle(int col, Raw<F32, 8>& r) const {
+    if constexpr (!VEC) {
+      const int early = col - (n - 8);
+      if (n >= 8 && early > 0) r = early < 8 ? moved_down(r, early) : Raw<F32, 8>{};
+    }
+  }
+  __device__ __forceinline__ Raw<F32, 8> settled(int col) const {
+    auto r = load(col);
+    settle(col, r);
+    return r;
+  }
+  __device__ __forceinline__ void store(int col, const Raw<F32, 8>& r) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < Raw<F32, 8>::N; i += 4)
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]}, buf, col * kBytes + 4 * i, 0, 2);
+    } else {
+      using T = std::conditional_t<F32, float, uint16_t>;
+      T* p = reinterpret_cast<T*>(base) + col;
+      if (n - col >= 8) {
+#pragma unroll
+        for (int i = 0; i < Raw<F32, 8>::N; i += 4)
+          *reinterpret_cast<Any16*>(reinterpret_cast<uint32_t*>(p) + i) = Any16{{r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]}};
+      } else if (n > col) {
+        st_part(p, r, n - col);
+      }
+    }
+  }
+};
 
 // Eight columns of the gain, float32 (lo, hi) or BF16 (lo), as they come.  The
 // type is a matter of uniform branches, which cost less than twice the kernels.
@@ -54,24 +138,28 @@ __device__ __forceinline__ Gain8 ld_gain8(const void* p, bool f32, int col, int 
   Gain8 g;
   g.hi = make_uint4(0, 0, 0, 0);
   if (f32) {
-    const auto r = ld_row8<true, VEC, true>(p, 0, col, n);
+    const auto r = Row<true, VEC>(p, 0, n).load(col);
     g.lo = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     g.hi = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
   } else {
-    const auto r = ld_row8<false, VEC, true>(p, 0, col, n);
+    const auto r = Row<false, VEC>(p, 0, n).load(col);
     g.lo = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
   }
   return g;
 }
-__device__ __forceinline__ void widen_gain8(const Gain8& g, bool f32, float* v) {
-  v[0] = f32 ? __uint_as_float(g.lo.x) : bf16_lo(g.lo.x);
-  v[1] = f32 ? __uint_as_float(g.lo.y) : bf16_hi(g.lo.x);
-  v[2] = f32 ? __uint_as_float(g.lo.z) : bf16_lo(g.lo.y);
-  v[3] = f32 ? __uint_as_float(g.lo.w) : bf16_hi(g.lo.y);
-  v[4] = f32 ? __uint_as_float(g.hi.x) : bf16_lo(g.lo.z);
-  v[5] = f32 ? __uint_as_float(g.hi.y) : bf16_hi(g.lo.z);
-  v[6] = f32 ? __uint_as_float(g.hi.z) : bf16_lo(g.lo.w);
-  v[7] = f32 ? __uint_as_float(g.hi.w) : bf16_hi(g.lo.w);
+template <bool VEC>
+__device__ __forceinline__ void widen_gain8(const Gain8& g, bool f32, int col, int n, float* v) {
+  if (f32) {
+    Raw<true, 8> r{{g.lo.x, g.lo.y, g.lo.z, g.lo.w, g.hi.x, g.hi.y, g.hi.z, g.hi.w}};
+    Row<true, VEC>(nullptr, 0, n).settle(col, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r.at(i);
+  } else {
+    Raw<false, 8> r{{g.lo.x, g.lo.y, g.lo.z, g.lo.w}};
+    Row<false, VEC>(nullptr, 0, n).settle(col, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r.at(i);
+  }
 }
 
 // y before its rounding to BF16.
@@ -124,6 +212,96 @@ __device__ __forceinline__ float reciprocal_rms(double sum, double inv_n, double
 #pragma unroll
   for (int i = 0; i < 2; ++i) y = __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
   return (float)y;
+}
+
+// Eight values of a row.
+template <bool F32>
+__device__ __forceinline__ void widen(const Raw<F32, 8>& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = r.at(i);
+}
+// Makes the compiler forget what it knows of r, so that a second use widens it
+// again: eight widened values kept between two uses take twice the registers
+// of eight BF16 ones.
+template <bool F32>
+__device__ __forceinline__ void forget(Raw<F32, 8>& r) {
+  if constexpr (!F32) asm volatile("" : "+v"(r.w[0]), "+v"(r.w[1]), "+v"(r.w[2]), "+v"(r.w[3]));
+}
+template <bool F32>
+__device__ __forceinline__ Raw<F32, 8> as_raw(const float* v) {
+  Raw<F32, 8> r;
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[i]);
+  } else {
+    const uint4 c = pack_bf16x8(v);
+    r.w[0] = c.x;
+    r.w[1] = c.y;
+    r.w[2] = c.z;
+    r.w[3] = c.w;
+  }
+  return r;
+}
+// Chunks of eight BF16 values, each quantized with the 16-lane DPP row that
+// holds its 1x128 tile; every lane of the wave takes part.  The scales of a
+// DPP row's CH tiles are worked out once, by lane u for tile u, as in the row
+// quantizer.
+template <bool POW2, bool VEC, int CH>
+__device__ __forceinline__ void encode_chunks(const uint4 (&d)[CH], uint32_t mine, int64_t row, int col0, int step, int n, uint8_t* codes,
+                                              int64_t ldc, float* scales) {
+  static_assert(CH == 1 || CH == 2 || CH == 4, "tiles u = 0 .. CH - 1 of a DPP row");
+  const int sub = threadIdx.x & 15, nb = (n + 127) >> 7;
+  const TileScale tm = tile_scale<POW2>(mine);
+  {
+    const int col = col0 - 8 * sub + sub * step;  // first column of tile `sub`
+    if (sub < CH && col < n) scales[row * nb + (col >> 7)] = tm.s;
+  }
+  uint8_t* out = codes + row * ldc;
+  __amdgpu_buffer_rsrc_t buf;
+  if constexpr (VEC) buf = __builtin_amdgcn_make_buffer_rsrc(out, 0, n, 0x00020000);
+  auto store = [&](int u, const TileScale& ts, auto enc) {
+    const uint2 c = enc(d[u], ts);
+    const int col = col0 + u * step, left = n - col;
+    if constexpr (VEC) {
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{c.x, c.y}, buf, col, 0, 2);
+    } else if (left >= 8) {
+      *reinterpret_cast<Any8*>(out + col) = Any8{{c.x, c.y}};
+    } else if (left > 0) {
+      store8_masked(out + col, c, left);
+    }
+  };
+  auto all = [&](auto enc) {
+    store(0, row_tile_scale<POW2, 0>(tm), enc);
+    if constexpr (CH > 1) store(1, row_tile_scale<POW2, 1>(tm), enc);
+    if constexpr (CH > 2) {
+      store(2, row_tile_scale<POW2, 2>(tm), enc);
+      store(3, row_tile_scale<POW2, 3>(tm), enc);
+    }
+  };
+  if constexpr (POW2) {
+    all([](uint4 x, const TileScale& t) { return encode8<true>(x, t); });
+  } else if (__builtin_amdgcn_ballot_w64(sub < CH && tm.slow) == 0) {  // (one wave-uniform decision)
+    all([](uint4 x, const TileScale& t) { return encode8_markstein<false>(x, t); });
+  } else {
+    all([](uint4 x, const TileScale& t) { return encode8_markstein<true>(x, t); });
+  }
+}
+
+// col0: the lane's first column, chunk u is u * step further.
+template <bool VEC, int CH>
+__device__ __forceinline__ void quantize_chunks(const uint4 (&d)[CH], bool pow2, int64_t row, int col0, int step, int n, uint8_t* codes,
+                                                int64_t ldc, float* scales) {
+  uint32_t mine = 0;  // lane u: tile u's max-abs
+#pragma unroll
+  for (int u = 0; u < CH; ++u) {
+    const uint32_t amax = dpp_max16(absmax8(d[u]));
+    mine = CH == 1 || (threadIdx.x & 15) == u ? amax : mine;
+  }
+  if (pow2) {
+    encode_chunks<true, VEC, CH>(d, mine, row, col0, step, n, codes, ldc, scales);
+  } else {
+    encode_chunks<false, VEC, CH>(d, mine, row, col0, step, n, codes, ldc, scales);
+  }
 }
 
 }  // namespace fp8q

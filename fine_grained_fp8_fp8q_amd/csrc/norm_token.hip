@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void norm_token_kernel(NormTokenArgs a, int nt
   const int col = f0 + 8 * c8, left = a.n - col;
   uint4 v[4];
   float w[8] = {};
-  if (left > 0) widen_gain8(ld_gain8<false>(a.weight, a.wf32, col, a.n), a.wf32, w);
+  if (left > 0) widen_gain8<false>(ld_gain8<false>(a.weight, a.wf32, col, a.n), a.wf32, col, a.n, w);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int t = t0 + 4 * q + p;

@@ -73,15 +73,17 @@ int main() {
 
   // backward: the workspace is what the launch will write, for every size that is accepted
   for (int64_t rows : {int64_t(0), int64_t(1), int64_t(31), int64_t(33), int64_t(5000), big})
-    for (int64_t n : {int64_t(1), int64_t(7), int64_t(512), int64_t(513), int64_t(1024), int64_t(2048), int64_t(2049), int64_t(7168), int64_t(16384),
+    for (int64_t n : {int64_t(1), int64_t(7), int64_t(512), int64_t(513), int64_t(1024), int64_t(2048), int64_t(2049), int64_t(7168), int64_t(8192), int64_t(8193), int64_t(16384),
                       int64_t(16385), int64_t(32768), int64_t(32769), row - 1}) {
       const int64_t need = fp8q_rmsnorm_backward_workspace(rows, n);
       CHECK(need % 16 == 0 && (need > 0) == (rows > 0));
-      if (rows > 0) {
-        const fp8q::NormBwdShape s = fp8q::norm_bwd_shape((int)rows, (int)n);
-        CHECK(need == s.blocks * fp8q::norm_partial_ld((int)n) * 4 && s.blocks >= 1 && s.blocks <= rows && fp8q::norm_partial_ld((int)n) >= n);
-        CHECK(s.threads >= 64 && s.threads <= 1024 && s.threads % 64 == 0);
-        CHECK(s.chunks == 0 ? n > 16384 : (int64_t)(s.wave ? 64 : s.threads) * s.chunks * 8 >= n);  // a row fits
+      for (bool f32 : {false, true}) {
+        if (rows == 0) break;
+        const fp8q::NormBwdShape s = fp8q::norm_bwd_shape((int)rows, (int)n, f32);
+        CHECK(need >= s.blocks * fp8q::norm_partial_ld((int)n) * 4 && s.blocks >= 1 && s.blocks <= rows && fp8q::norm_partial_ld((int)n) >= n);
+        CHECK(s.threads >= 64 && s.threads <= (s.chunks ? s.wave ? 256 : 512 : 1024) && s.threads % 64 == 0);
+        CHECK(s.chunks == 0 ? n > (f32 ? 8192 : 16384) : (int64_t)(s.wave ? 64 : s.threads) * s.chunks * 8 >= n);  // a row fits
+        CHECK(s.chunks <= (f32 ? 2 : 4) && (s.wave || s.chunks == 0 || s.chunks == (f32 ? 2 : 4)));  // the kernels there are
       }
       if (need > 0) {
         CHECK(fp8q_rmsnorm_backward(P, 1, rows, n, n, P, 1, n, F, P, 1, nullptr, 0, P, 1, n, 0, nullptr, 0, nullptr, F, P, need - 1, nullptr) == FP8Q_ERR_INVALID_ARG);
