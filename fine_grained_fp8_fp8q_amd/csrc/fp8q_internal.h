@@ -258,6 +258,10 @@ constexpr int kMaxGateExperts = 512;
 constexpr int kMaxGateChoices = 64;  // one lane each
 constexpr int kMaxGateGroups = 64;
 constexpr int kMaxGateGrid = 1 << 20;
+struct GateSplit {
+  int lane_bits, per;  // lanes of a group (their log2), experts of a lane
+  bool fits;
+};
 struct GateArgs {
   const void* logits;
   int64_t ld;
@@ -268,7 +272,8 @@ struct GateArgs {
   int* load;      // null: not counted
   double scale;
   int tokens, experts, topk, groups, top_groups;
-  int group_lanes;  // (set by the launcher)
+  int per_group;           // (set by the launcher, as the splits
+  GateSplit wide, narrow;  // of 64 and 16 lanes a token)
   bool lf32, i64, sigmoid, two_best, renormalize;
 };
 hipError_t launch_gate(GateArgs a, hipStream_t stream);

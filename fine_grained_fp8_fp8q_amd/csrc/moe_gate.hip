@@ -12,8 +12,8 @@
 // An expert whose logit or bias is -inf or NaN is never chosen; where fewer
 // than topk are left, the rest of the row is -1 with weight 0 (a row of the
 // table without an expert, which the sort drops and the weighted sum skips).
+#include "chunk8.h"
 #include "fp8q_internal.h"
-#include "quant_common.h"
 
 namespace fp8q {
 namespace {
@@ -29,125 +29,496 @@ __device__ __forceinline__ float ld_logit(const void* p, bool f32, int64_t i) {
 // A logit as it is used: NaN is none (-inf), +inf the largest number.
 __device__ __forceinline__ double as_logit(float x) { return x == x ? (double)fminf(x, 3.402823466e38f) : kNone; }
 
-__device__ __forceinline__ double gate_sum(double v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+// The value of another lane of the same 16, by a DPP control.
+template <int CTRL>
+__device__ __forceinline__ double gate_dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double gate_lane(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// f over a token's L lanes (16: one DPP row, or the whole wave), the same in
+// each.  All 64 lanes must be active.
+template <int L, class F>
+__device__ __forceinline__ double gate_all(double v, F f) {
+  v = f(v, gate_dpp<0xB1>(v));
+  v = f(v, gate_dpp<0x4E>(v));
+  v = f(v, gate_dpp<0x141>(v));
+  v = f(v, gate_dpp<0x140>(v));
+  if constexpr (L == 64) v = f(f(gate_lane(v, 0), gate_lane(v, 16)), f(gate_lane(v, 32), gate_lane(v, 48)));
   return v;
 }
+template <int L>
+__device__ __forceinline__ double gate_sum(double v) {
+  return gate_all<L>(v, [](double x, double y) { return x + y; });
+}
+template <int L>
 __device__ __forceinline__ double gate_max(double v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = fmax(v, __shfl_xor(v, d));
-  return v;
+  return gate_all<L>(v, [](double x, double y) { return fmax(x, y); });
+}
+
+// exp(x) in 64 bits: x = k ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, so
+// that k times the first is exact), the exponential series up to r^13 / 13!
+// (the next term is below 2^-57), times 2^k.  Within 2 ulps; 0 and infinity
+// where the result leaves the range.
+__device__ __forceinline__ double exp64(double x) {
+  x = fmin(fmax(x, -1100.0), 1100.0);
+  const double k = __builtin_rint(x * 0x1.71547652b82fep+0);
+  double r = __builtin_fma(-k, 0x1.62e42fefap-1, x);
+  r = __builtin_fma(-k, 0x1.cf79abc9e3b3ap-40, r);
+  double p = 1.0 / 6227020800.0;
+  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)k);
 }
 
 // Score of a logit; softmax: top the row's largest, inv 1 / sum exp(x - top).
 __device__ __forceinline__ double score_of(double x, bool sigmoid, double top, double inv) {
-  if (sigmoid) return 1.0 / (1.0 + exp(-x));
-  return x > kNone ? exp(x - top) * inv : 0.0;
+  if (sigmoid) return 1.0 / (1.0 + exp64(-x));
+  return x > kNone ? exp64(x - top) * inv : 0.0;
 }
 
-// One wave per token.  The lanes are shared out evenly over the groups (64 /
-// the power of two above them each), a lane holds consecutive experts of its
-// group, so a lower lane's experts come before a higher one's.
+// The same for a float32 result: the hardware's estimate of the reciprocal and
+// two Newton steps, a third of the division's instructions (a score below
+// e^-120 is 0 in float32 either way).
+__device__ __forceinline__ float score32(double x, bool sigmoid, double top, double inv) {
+  if (!sigmoid) return x > kNone ? (float)(exp64(x - top) * inv) : 0.0f;
+  const double d = 1.0 + exp64(fmin(-x, 120.0));
+  double y = __builtin_amdgcn_rcp(d);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  return (float)y;
+}
+
+// The lanes of a token, L of them, are shared out evenly over the groups (L /
+// the power of two above them each); a lane holds up to P consecutive experts
+// of its group, by fours, so a lower lane's experts come before a higher one's.
+template <int L, int P>
+struct GateLane {
+  int lane, lpg, group, base, mine;  // lpg: lanes of a group; base, mine: the lane's first expert and their number
+  bool fours;                        // groups of whole fours
+  __device__ __forceinline__ explicit GateLane(const GateArgs& a) {
+    const GateSplit& s = L == 64 ? a.wide : a.narrow;
+    lane = threadIdx.x & (L - 1);
+    lpg = 1 << s.lane_bits;
+    const int first = (lane & (lpg - 1)) * s.per;
+    group = lane >> s.lane_bits;
+    base = group * a.per_group + first;
+    mine = group < a.groups ? min(max(a.per_group - first, 0), s.per) : 0;
+    fours = a.per_group % 4 == 0;
+  }
+  // The lane's values of a row; those it does not have are the row's last.
+  __device__ __forceinline__ void load(const void* p, bool f32, int64_t row, int experts, float (&f)[P]) const {
+    int base = this->base;
+    asm volatile("" : "+v"(base));  // (or an offset for every value is kept from turn to turn)
+    if (!fours) {
+#pragma unroll
+      for (int c = 0; c < P; ++c) f[c] = ld_logit(p, f32, row + min(base + c, experts - 1));
+    } else if (f32) {
+#pragma unroll
+      for (int c = 0; c < P; c += 4) {
+        const auto r = ld_raw<true, 4, true>(p, row + min(base + c, experts - 4), 4, false);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[c + i] = r.at(i);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < P; c += 4) {
+        const auto r = ld_raw<false, 4, true>(p, row + min(base + c, experts - 4), 4, false);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[c + i] = r.at(i);
+      }
+    }
+  }
+};
+
+// The largest of N values, as a tree.
+template <int N, class T, class F>
+__device__ __forceinline__ T gate_tree(const T* v, F f) {
+  if constexpr (N == 1) {
+    return v[0];
+  } else {
+    return f(gate_tree<N / 2>(v, f), gate_tree<N - N / 2>(v + N / 2, f));
+  }
+}
+template <int N>
+__device__ __forceinline__ double gate_tree_max(const double* v) {
+  return gate_tree<N>(v, [](double x, double y) { return fmax(x, y); });
+}
+
+// What lane j of a token's lanes does with its j-th expert (-1: none).
+template <int L>
+__device__ __forceinline__ void gate_write(const GateArgs& a, int64_t t, bool real, int lane, int chosen, double w) {
+  if (a.renormalize) {
+    const double total = gate_sum<L>(w);
+    w = total > 0.0 ? w / total : 0.0;
+  }
+  if (real && lane < a.topk) {
+    const int64_t at = t * a.topk + lane;
+    if (a.i64) {
+      static_cast<int64_t*>(a.chosen)[at] = chosen;
+    } else {
+      static_cast<int32_t*>(a.chosen)[at] = chosen;
+    }
+    a.weights[at] = (float)(a.scale * w);
+    if (a.load && chosen >= 0) atomicAdd(a.load + chosen, 1);
+  }
+}
+
+// One token by a whole wave, every step in 64 bits.
 template <int P>
-__global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int per_group = a.experts / a.groups;
-  const int lpg = 64 / a.group_lanes;  // (group_lanes: the power of two)
-  const int per = (per_group + lpg - 1) / lpg;
-  const int group = lane / lpg, first = (lane % lpg) * per;
-  const int base = group * per_group + first;
-  const int mine = group < a.groups ? min(max(per_group - first, 0), per) : 0;  // experts of this lane
-  for (int t = (int)blockIdx.x * kGateWaves + (int)(threadIdx.x >> 6); t < a.tokens; t += (int)gridDim.x * kGateWaves) {
-    const int64_t row = (int64_t)t * a.ld;
-    double x[P], key[P];
+__device__ __forceinline__ void gate_exact(const GateArgs& a, int64_t t) {
+  const GateLane<64, P> at(a);
+  const int64_t row = t * a.ld;
+  float f[P];
+  at.load(a.logits, a.lf32, row, a.experts, f);
+  double x[P], key[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) x[p] = p < mine ? as_logit(ld_logit(a.logits, a.lf32, row + base + p)) : kNone;
-    double top = kNone, inv = 0.0;
-    if (!a.sigmoid) {
+  for (int p = 0; p < P; ++p) x[p] = p < at.mine ? as_logit(f[p]) : kNone;
+  double top = kNone, inv = 0.0;
+  if (!a.sigmoid) {
+    top = gate_max<64>(gate_tree_max<P>(x));
+    double total = 0.0;
 #pragma unroll
-      for (int p = 0; p < P; ++p) top = fmax(top, x[p]);
-      top = gate_max(top);
-      double total = 0.0;
+    for (int p = 0; p < P; ++p)
+      if (x[p] > kNone) total += exp64(x[p] - top);
+    total = gate_sum<64>(total);
+    inv = total > 0.0 ? 1.0 / total : 0.0;
+  }
+  // scores where something asks for them; the choice is by x without a bias
+  if (a.bias || a.scores || a.groups > 1) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) key[p] = score_of(x[p], a.sigmoid, top, inv);
+    if (a.scores) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        if (x[p] > kNone) total += exp(x[p] - top);
-      total = gate_sum(total);
-      inv = total > 0.0 ? 1.0 / total : 0.0;
+        if (p < at.mine) a.scores[t * a.experts + at.base + p] = (float)key[p];
     }
+    if (a.bias) {
+      at.load(a.bias, true, 0, a.experts, f);
+#pragma unroll
+      for (int p = 0; p < P; ++p) key[p] = key[p] + (double)f[p];
+    }
+  }
+  if (a.groups > 1) {
+    // the group's best and second best
+    const bool by_key = a.bias || a.two_best;
+    double b1 = kNone, b2 = kNone;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const double s = score_of(x[p], a.sigmoid, top, inv);
-      if (a.scores && p < mine) a.scores[(int64_t)t * a.experts + base + p] = (float)s;
-      key[p] = x[p];
-      if (p < mine && a.bias && x[p] > kNone) {
-        const double k = s + (double)a.bias[base + p];
-        key[p] = k > kNone ? k : kNone;
-      }
+      double k = by_key ? key[p] : x[p];
+      k = x[p] > kNone && k > kNone ? k : kNone;
+      b2 = fmax(b2, fmin(b1, k));
+      b1 = fmax(b1, k);
     }
-    if (a.groups > 1) {
-      // the group's best and second best; two best: of their scores
-      double b1 = kNone, b2 = kNone;
+    for (int d = 1; d < at.lpg; d <<= 1) {
+      const double o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+      b2 = fmax(fmax(b2, o2), fmin(b1, o1));
+      b1 = fmax(b1, o1);
+    }
+    if (a.two_best && b2 > kNone) b1 += b2;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double o = __shfl(b1, g * at.lpg);
+      before += o > b1 || (o == b1 && g < at.group);
+    }
+    if (before >= a.top_groups) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) x[p] = kNone;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const double k = a.bias ? key[p] : x[p];
+    key[p] = x[p] > kNone && k > kNone ? k : kNone;  // (a bias of NaN too)
+  }
+  // topk rounds; lane j keeps the j-th expert
+  int chosen = -1;
+  for (int j = 0; j < a.topk; ++j) {
+    const double best = gate_tree_max<P>(key), all = gate_max<64>(best);
+    // the lowest lane that holds it
+    const uint64_t have = __builtin_amdgcn_ballot_w64(best == all && all > kNone);
+    if (have == 0) break;
+    const int owner = __builtin_ctzll(have);
+    int e = 0;
+#pragma unroll
+    for (int p = P - 1; p >= 0; --p)
+      if (key[p] == all) e = p;
+    if (at.lane == owner) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (p == e) key[p] = kNone;
+    }
+    e = __builtin_amdgcn_readlane(at.base + e, owner);
+    if (at.lane == j) chosen = e;
+  }
+  double w = 0.0;
+  if (chosen >= 0) w = score_of(as_logit(ld_logit(a.logits, a.lf32, row + chosen)), a.sigmoid, top, inv);
+  gate_write<64>(a, t, true, at.lane, chosen, w);
+}
+template <int P>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_exact_kernel(GateArgs a) {
+  const int64_t stride = (int64_t)gridDim.x * kGateWaves;
+  for (int64_t t = (int64_t)blockIdx.x * kGateWaves + (int)(threadIdx.x >> 6); t < a.tokens; t += stride) gate_exact<P>(a, t);
+}
+
+// The middle one of three (one instruction).
+__device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) { return max(min(a, b), min(max(a, b), c)); }
+template <int L>
+__device__ __forceinline__ uint32_t gate_max_u32(uint32_t v) {
+  v = dpp_max16(v);
+  if constexpr (L == 64) {
+    v = max(max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
+            max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t gate_min_u32(uint32_t v) {
+  return ~gate_max_u32<L>(~v);
+}
+// Order of float32 values as unsigned ones, NaN aside.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
+
+// The choice by float32 scores where these are enough to know the 64-bit
+// order, which is nearly always: a third of the instructions, and short ones.
+// L lanes a token, 64 / L tokens a wave.
+//
+// Every open expert gets a 32-bit key, the lowest the best: d = the row's
+// highest float32 score less its own, whose bits order like the number, with
+// the index in the place of its last nine bits, so that keys differ and equal
+// scores go by index.  Close to the highest, where it matters, d is finest.  A
+// lane keeps its T best keys in order (a minimum and T - 1 medians of three per
+// expert); rounds take the best head of all lanes.  The float32 score is within
+// err of the 64-bit one:
+//   sigmoid, u = 2^-24: 0.4 u of the exponent's rounding (1.5 u |x|, times s
+//     (1 - s), with |x| s (1 - s) < 0.23), 0.5 u of exp2 (an ulp, times s (1 -
+//     s)), u of the sum, 2 u of the reciprocal (an ulp): below 6 u;
+//   softmax: its numerator 1 u (2.5 u |d|, d = x - top, with |d| e^-|d| < 0.37)
+//     and 2 u; the denominator 2.5 u times the mean |d|, at most ln 512, 2 u of
+//     exp2, 15 u of a lane's sum, u of its rounding, 2 u of the reciprocal, and
+//     u of the product, each times s <= 1: below 48 u;
+//   the sum with the bias u of it, and d u of that: 2 u of the largest.
+// so two experts whose d differ by more than 2 err and the nine bits are in
+// order.  Without a bias d comes from the logits themselves and never reverses
+// them: any two different keys are in order if the logits differ at all.  Two more experts than asked for are taken.  If neighbours among them are
+// not clear of one another, their 64-bit scores rank them; if the last one
+// chosen is not clear of the last one taken, somebody left out might belong in,
+// and the wave does the token in 64 bits.  So it does if groups are not clear
+// of one another or a lane's list ran out.
+enum { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };  // what is chosen by: x, or the score with a bias
+template <int L, int P, int BY>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
+  constexpr int kTokens = 64 / L;         // of a wave
+  constexpr int T = P < 8 ? P : 8;        // experts in a lane's list
+  constexpr int kExactP = L == 64 ? P : 4;  // a quarter of P where four times the lanes share a token
+  constexpr float U = 0x1p-24f, kLow = -__builtin_inff(), kLog2e = 1.44269504f;
+  constexpr uint32_t kNoKey = 0xFFFFFFFFu;
+  const GateLane<L, P> at(a);
+  const int lane = at.lane, sub = (threadIdx.x & 63) / L, taken = a.topk + 2;
+  const int64_t stride = (int64_t)gridDim.x * kGateWaves * kTokens;
+  // (whole waves go round together; a token past the last is worked on as the last)
+  for (int64_t t0 = ((int64_t)blockIdx.x * kGateWaves + (int)(threadIdx.x >> 6)) * kTokens; t0 < a.tokens; t0 += stride) {
+    const bool real = t0 + sub < a.tokens;
+    const int64_t t = real ? t0 + sub : a.tokens - 1;
+    const int64_t row = t * a.ld;
+    float x[P], key[P], bias[P];
+    at.load(a.logits, a.lf32, row, a.experts, x);
+    if constexpr (BY != kByLogit) at.load(a.bias, true, 0, a.experts, bias);
+    int mine = at.mine;
+    asm volatile("" : "+v"(mine));  // (or a mask for every p is kept from turn to turn)
+#pragma unroll
+    for (int p = 0; p < P; ++p) x[p] = ((p < mine) & (x[p] == x[p])) ? fminf(x[p], 3.402823466e38f) : kLow;
+    float top = kLow, err = 0.0f;
+    if (BY == kBySoftmax || !a.sigmoid) {
+      top = gate_tree<P>(x, [](float u, float v) { return fmaxf(u, v); });
+      top = unordered(gate_max_u32<L>(ordered(top)));
+    }
+    if constexpr (BY == kByLogit) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) key[p] = x[p];
+    } else if constexpr (BY == kBySigmoid) {
+      err = 6.0f * U;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        double k = key[p];
-        if (a.two_best && !a.bias && k > kNone) k = score_of(x[p], a.sigmoid, top, inv);
-        b2 = fmax(b2, fmin(b1, k));
-        b1 = fmax(b1, k);
+        const float k = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[p] * kLog2e)) + bias[p];
+        key[p] = ((x[p] > kLow) & (bias[p] > kLow)) ? k : kLow;
       }
-      for (int d = 1; d < lpg; d <<= 1) {
-        const double o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
-        b2 = fmax(fmax(b2, o2), fmin(b1, o1));
-        b1 = fmax(b1, o1);
+    } else {
+      err = 48.0f * U;
+      float total = 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float e = __builtin_amdgcn_exp2f((x[p] - top) * kLog2e);  // (a NaN in a row of -inf)
+        key[p] = x[p] > kLow ? e : 0.0f;
+        total += key[p];
       }
-      if (a.two_best && b2 > kNone) b1 += b2;
+      total = (float)gate_sum<L>((double)total);
+      const float inv = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float k = key[p] * inv + bias[p];
+        key[p] = ((x[p] > kLow) & (bias[p] > kLow)) ? k : kLow;
+      }
+    }
+    bool unsure = false;
+    if (a.groups > 1) {
+      // the group's best and second best
+      float b1 = kLow, b2 = kLow;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        b2 = fmaxf(b2, fminf(b1, key[p]));
+        b1 = fmaxf(b1, key[p]);
+      }
+      for (int d = 1; d < at.lpg; d <<= 1) {
+        const float o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+        b1 = fmaxf(b1, o1);
+      }
+      const float rank = a.two_best && b2 > kLow ? b1 + b2 : b1;
       int before = 0;
       for (int g = 0; g < a.groups; ++g) {
-        const double o = __shfl(b1, g * lpg);
-        before += o > b1 || (o == b1 && g < group);
+        const float o = __shfl(rank, g * at.lpg, L);
+        before += o > rank || (o == rank && g < at.group);
       }
-      if (before >= a.top_groups) {
+      const bool open = before < a.top_groups;
+      if constexpr (BY != kByLogit) {
+        // every closed group has to be clear of every open one (two scores are
+        // added to two biases, and the sums)
+        const float off = 2.0f * err + 4.0f * U * ((b1 > kLow ? fabsf(b1) : 0.0f) + (b2 > kLow ? fabsf(b2) : 0.0f));
+        const bool real_group = at.group < a.groups;
+        const float in = -unordered(gate_max_u32<L>(ordered(open && real_group ? off - rank : kLow)));
+        const float out = unordered(gate_max_u32<L>(ordered(!open && real_group ? rank + off : kLow)));
+        unsure = !(off < 1e38f) || (out > kLow && !(in > out));
+      }
+      if (!open) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) key[p] = kNone;
+        for (int p = 0; p < P; ++p) key[p] = kLow;
       }
     }
-    // topk rounds; lane j keeps the j-th expert
-    int chosen = -1;
-    for (int j = 0; j < a.topk; ++j) {
-      double best = kNone;
+    float high = gate_tree<P>(key, [](float u, float v) { return fmaxf(u, v); });
+    high = unordered(gate_max_u32<L>(ordered(high)));
+    if constexpr (BY != kByLogit) unsure = unsure || high > 1e38f;  // (a bias beyond scores)
+    uint32_t m[T];
 #pragma unroll
-      for (int p = 0; p < P; ++p) best = fmax(best, key[p]);
-      const double all = gate_max(best);
-      const uint64_t have = __builtin_amdgcn_ballot_w64(best == all && all > kNone);
-      if (have == 0) break;
-      const int owner = __builtin_ctzll(have);
-      int e = -1;
+    for (int i = 0; i < T; ++i) m[i] = kNoKey;
+    int first = at.base;
+    asm volatile("" : "+v"(first));
 #pragma unroll
-      for (int p = P - 1; p >= 0; --p)
-        if (key[p] == all) e = p;
-      if (lane == owner) {
+    for (int p = 0; p < P; ++p) {
+      const uint32_t d = (__float_as_uint(high - key[p]) & ~511u) | (uint32_t)(first + p);
+      const uint32_t k = key[p] > kLow ? d : kNoKey;
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          if (p == e) key[p] = kNone;
-      }
-      e = __shfl(base + e, owner);
-      if (lane == j) chosen = e;
+      for (int i = T - 1; i > 0; --i)
+        if (i <= p) m[i] = i < p ? med3(m[i - 1], m[i], k) : max(m[i - 1], k);
+      m[0] = min(m[0], k);
     }
-    double w = 0.0;
-    if (chosen >= 0) w = score_of(as_logit(ld_logit(a.logits, a.lf32, row + chosen)), a.sigmoid, top, inv);
-    if (a.renormalize) {
-      const double total = gate_sum(w);
-      w = total > 0.0 ? w / total : 0.0;
+    uint32_t cand = kNoKey;  // lane j: the j-th best key
+    int popped = 0;
+    for (int j = 0; j < taken; ++j) {
+      const uint32_t all = gate_min_u32<L>(m[0]);
+      const uint32_t won = ((m[0] == all) & (all != kNoKey)) ? ~0u : 0u;
+      cand = lane == j ? all : cand;
+      // the winner's list moves up (by masks: of selects the compiler makes an indexed array)
+#pragma unroll
+      for (int i = 0; i + 1 < T; ++i) m[i] = (m[i + 1] & won) | (m[i] & ~won);
+      m[T - 1] |= won;
+      popped -= (int)won;
     }
-    if (lane < a.topk) {
-      const int64_t at = (int64_t)t * a.topk + lane;
-      if (a.i64) {
-        static_cast<int64_t*>(a.chosen)[at] = chosen;
-      } else {
-        static_cast<int32_t*>(a.chosen)[at] = chosen;
+    if (P > T) unsure = unsure || (popped >= T && at.mine > T);
+    int chosen = cand != kNoKey ? (int)(cand & 511u) : -1;
+    float logit = 0.0f;
+    if (chosen >= 0) logit = ld_logit(a.logits, a.lf32, row + chosen);
+    // whether an expert of key `far` is certainly behind one of key `near`
+    const float most = 2.0f * err + 4.0f * U * fabsf(high);  // (and of what lies below, with its d)
+    auto behind = [&](uint32_t near, uint32_t far) {
+      const float dn = __uint_as_float(near & ~511u), df = __uint_as_float(far & ~511u);
+      if constexpr (BY == kByLogit) return df > dn;
+      return df - dn > most + df * 0x1p-12f;
+    };
+    // neighbours: lane j and j + 1
+    const uint32_t next = (uint32_t)__shfl_down((int)cand, 1, L), last = (uint32_t)__shfl((int)cand, taken - 1, L);
+    const float logit_next = __shfl_down(logit, 1, L);
+    bool close = lane < a.topk && next != kNoKey && !behind(cand, next);
+    if (BY == kByLogit) close = close && logit != logit_next;  // (equal logits go by index)
+    const uint64_t any_close = __builtin_amdgcn_ballot_w64(close);
+    double s_top = kNone, s_inv = 0.0;
+    if (!a.sigmoid) {
+      // the 64-bit denominator where it is asked for
+      s_top = as_logit(top);
+      s_inv = 1.0;
+      if (!a.renormalize || a.scores || any_close) {
+        // (four experts at a time, from the cache: all side by side their steps would
+        // fill the registers of every call)
+        double total = 0.0;
+        for (int p0 = 0; p0 < mine; p0 += 4) {
+          double e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = exp64(as_logit(ld_logit(a.logits, a.lf32, row + first + min(p0 + i, mine - 1))) - s_top);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) total += p0 + i < mine ? e[i] : 0.0;
+        }
+        total = gate_sum<L>(total);
+        s_inv = total > 0.0 ? 1.0 / total : 0.0;
       }
-      a.weights[at] = (float)(a.scale * w);
-      if (a.load && chosen >= 0) atomicAdd(a.load + chosen, 1);
+    }
+    if (a.scores && real) {
+      float* out = a.scores + t * a.experts + first;
+      for (int p0 = 0; p0 < mine; p0 += 4) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = score32(as_logit(ld_logit(a.logits, a.lf32, row + first + min(p0 + i, mine - 1))), a.sigmoid, s_top, s_inv);
+        st_float4(out + p0, v, mine - p0, false);
+      }
+    }
+    double s = chosen >= 0 ? score_of(as_logit(logit), a.sigmoid, s_top, s_inv) : 0.0;
+    if (any_close) {
+      // the taken ones in their 64-bit order
+      const double k = chosen < 0 ? kNone : BY == kByLogit ? as_logit(logit) : s + (double)a.bias[chosen];
+      int place = 0;
+      for (int j = 0; j < taken; ++j) {
+        const double kj = __shfl(k, j, L);
+        const int ej = __shfl(chosen, j, L);
+        place += kj > k || (kj == k && ej >= 0 && ej < chosen);
+      }
+      int from = lane;  // lane j takes the one whose place is j
+      for (int j = 0; j < taken; ++j) {
+        if (__shfl(place, j, L) == lane) from = j;
+      }
+      chosen = __shfl(chosen, from, L);
+      s = __shfl(s, from, L);
+      cand = (uint32_t)__shfl((int)cand, from, L);
+    }
+    // the chosen ones have to be clear of whatever was left out, all of it behind the last one taken
+    unsure = unsure || (lane < a.topk && cand != kNoKey && last != kNoKey && !behind(cand, last));
+    const uint64_t redo = __builtin_amdgcn_ballot_w64(unsure);
+    auto again = [&](int i) { return (redo >> (i * L & 63) & (~0ull >> (64 - L))) != 0; };  // token i of the wave
+    gate_write<L>(a, t, real && !again(sub), lane, lane < a.topk ? chosen : -1, lane < a.topk ? s : 0.0);
+    if (redo) {
+      for (int i = 0; i < kTokens && t0 + i < a.tokens; ++i)
+        if (again(i)) gate_exact<kExactP>(a, t0 + i);
     }
   }
 }
@@ -164,13 +535,13 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_kernel(GateBwdArgs a
     double top = kNone, inv = 0.0;
     if (!a.sigmoid) {
       for (int e = lane; e < a.experts; e += 64) top = fmax(top, logit(e));
-      top = gate_max(top);
+      top = gate_max<64>(top);
       double total = 0.0;
       for (int e = lane; e < a.experts; e += 64) {
         const double x = logit(e);
-        if (x > kNone) total += exp(x - top);
+        if (x > kNone) total += exp64(x - top);
       }
-      total = gate_sum(total);
+      total = gate_sum<64>(total);
       inv = total > 0.0 ? 1.0 / total : 0.0;
     }
     // lane j: the j-th choice
@@ -186,7 +557,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_kernel(GateBwdArgs a
     }
     if (a.renormalize) {
       const double s = e >= 0 ? score_of(logit(e), a.sigmoid, top, inv) : 0.0;
-      const double total = gate_sum(s), dot = gate_sum(e >= 0 ? ds * s : 0.0);
+      const double total = gate_sum<64>(s), dot = gate_sum<64>(e >= 0 ? ds * s : 0.0);
       ds = total > 0.0 ? (ds - dot / total) / total : 0.0;
     }
     ds *= a.scale;
@@ -206,12 +577,12 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_kernel(GateBwdArgs a
         const double x = logit(i), d = grad(i) * score_of(x, false, top, inv);
         if (e0 + lane < a.experts && x > kNone) mean += d;
       }
-      mean = gate_sum(mean);
+      mean = gate_sum<64>(mean);
     }
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
       const int i = min(e0 + lane, a.experts - 1);
       const double x = logit(i), s = score_of(x, a.sigmoid, top, inv);
-      double d = a.sigmoid ? grad(i) * s * (1.0 / (1.0 + exp(x))) : s * (grad(i) - mean);
+      double d = a.sigmoid ? grad(i) * s * (1.0 / (1.0 + exp64(x))) : s * (grad(i) - mean);
       if (!(x > kNone)) d = 0.0;
       if (e0 + lane < a.experts) {
         const int64_t at = (int64_t)t * a.ldd + i;
@@ -225,19 +596,62 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_kernel(GateBwdArgs a
   }
 }
 
-int gate_grid(int tokens) {
-  const int want = (tokens + kGateWaves - 1) / kGateWaves;
-  return want < kMaxGateGrid ? want : kMaxGateGrid;
+int gate_grid(int64_t waves) {
+  const int64_t want = (waves + kGateWaves - 1) / kGateWaves;
+  return (int)(want < kMaxGateGrid ? want : kMaxGateGrid);
 }
 
 }  // namespace
 
+template <int L, int BY>
+static void launch_gate_by(const GateArgs& a, int per, hipStream_t stream) {
+  auto kernel = per <= 4 ? gate_kernel<L, 4, BY> : per <= 8 ? gate_kernel<L, 8, BY> : gate_kernel<L, kGateLane, BY>;
+  const int64_t waves = ((int64_t)a.tokens * L + 63) / 64;
+  hipLaunchKernelGGL(kernel, dim3(gate_grid(waves)), dim3(64 * kGateWaves), 0, stream, a);
+}
+template <int L>
+static void launch_gate_lanes(const GateArgs& a, int per, hipStream_t stream) {
+  if (!a.bias) {
+    launch_gate_by<L, kByLogit>(a, per, stream);
+  } else if (a.sigmoid) {
+    launch_gate_by<L, kBySigmoid>(a, per, stream);
+  } else {
+    launch_gate_by<L, kBySoftmax>(a, per, stream);
+  }
+}
+
+// Four tokens a wave take less time in all, one a wave less for each: of 256
+// experts, 2048 tokens 8.2 against 7.3 us, 4096 9.1 against 9.3, 16384 14.0
+// against 21.9; of 60, 1024 tokens 4.2 against 4.3, 16384 6.2 against 15.0.  The
+// scores of all experts, which are written in 64-bit steps, are many for a lane
+// of few: 4099 tokens of 160 14.3 against 12.0, 16384 24.9 against 29.0.
+static int gate_narrow_from(const GateArgs& a) { return a.scores ? 16384 : a.narrow.per <= 8 ? 1024 : 4096; }
+
+// How `lanes` lanes a token share out the experts (GateLane).
+static GateSplit gate_split(const GateArgs& a, int lanes) {
+  GateSplit s{};
+  int groups = 1;
+  while (groups < a.groups) groups *= 2;
+  while ((groups << s.lane_bits) < lanes) ++s.lane_bits;
+  s.per = (a.per_group + (1 << s.lane_bits) - 1) >> s.lane_bits;
+  s.per = (s.per + 3) / 4 * 4;
+  s.fits = groups <= lanes && s.per <= kGateLane;
+  return s;
+}
+
 hipError_t launch_gate(GateArgs a, hipStream_t stream) {
-  a.group_lanes = 1;
-  while (a.group_lanes < a.groups) a.group_lanes *= 2;
-  const int lpg = 64 / a.group_lanes, per = (a.experts / a.groups + lpg - 1) / lpg;
-  auto kernel = per <= 1 ? gate_kernel<1> : per <= 2 ? gate_kernel<2> : per <= 4 ? gate_kernel<4> : per <= 8 ? gate_kernel<8> : gate_kernel<kGateLane>;
-  hipLaunchKernelGGL(kernel, dim3(gate_grid(a.tokens)), dim3(64 * kGateWaves), 0, stream, a);
+  a.per_group = a.experts / a.groups;
+  a.wide = gate_split(a, 64);
+  a.narrow = gate_split(a, 16);
+  if (a.topk + 2 > 64 || (a.groups > 1 && a.two_best && !a.bias)) {
+    // (no lane for each expert taken, two more than asked for; groups by scores, experts by logits)
+    auto kernel = a.wide.per <= 4 ? gate_exact_kernel<4> : a.wide.per <= 8 ? gate_exact_kernel<8> : gate_exact_kernel<kGateLane>;
+    hipLaunchKernelGGL(kernel, dim3(gate_grid(a.tokens)), dim3(64 * kGateWaves), 0, stream, a);
+  } else if (a.narrow.fits && a.topk + 2 <= 16 && a.tokens >= gate_narrow_from(a)) {
+    launch_gate_lanes<16>(a, a.narrow.per, stream);
+  } else {
+    launch_gate_lanes<64>(a, a.wide.per, stream);
+  }
   return hipGetLastError();
 }
 

@@ -13,6 +13,7 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 # a float64 value rounded to float32: half a step; the 64-bit steps before it are far below a tenth of that
 NEAR32 = 1.1 * 2.0 ** -24
+MANY = 16400  # tokens from which every choice of kernels is that of large batches
 
 
 @pytest.fixture(autouse=True)
@@ -52,6 +53,18 @@ def check(x, dtype, topk, bias=None, pad=0, index_dtype=torch.int32, **kw):
     assert np.array_equal(host(load) - 5, np.bincount(we[we >= 0], minlength=x.shape[1]))
     e, w, s = fp8q.moe_route(on(x, dtype, pad), topk, bias=bd, **kw)
     assert s is None and np.array_equal(host(e), we) and (np.abs(host(w.double()) - ww) <= NEAR32 * ww + 2.0 ** -149).all()
+    # the same tokens over and over, by the kernels of many tokens (and a last wave that is not full)
+    times = -(-MANY // x.shape[0])
+    rows = torch.arange(times * x.shape[0] - 1, device="cuda:0") % x.shape[0]
+    many = on(x, dtype, pad)[rows]
+    bound = dev(NEAR32 * ww + 2.0 ** -149)[rows]
+    for want_scores in (False, True):
+        load.zero_()
+        e, w, s = fp8q.moe_route(many, topk, bias=bd, load=load, want_scores=want_scores, **kw)
+        assert torch.equal(e, dev(we)[rows].int()) and bool(((w.double() - dev(ww)[rows]).abs() <= bound).all())
+        assert torch.equal(load, torch.bincount(e[e >= 0].long(), minlength=x.shape[1]).int())
+        if want_scores:
+            assert bool(((s.double() - dev(ws)[rows]).abs() <= NEAR32 * dev(ws)[rows] + 2.0 ** -149).all())
 
 
 # experts, groups, open groups, topk
