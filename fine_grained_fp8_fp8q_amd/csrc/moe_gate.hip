@@ -164,6 +164,12 @@ __device__ __forceinline__ double gate_tree_max(const double* v) {
   return gate_tree<N>(v, [](double x, double y) { return fmax(x, y); });
 }
 
+// What the lanes of a wave have written to LDS is there for one another.
+__device__ __forceinline__ void gate_wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // What lane j of a token's lanes does with its j-th expert (-1: none).
 template <int L>
 __device__ __forceinline__ void gate_write(const GateArgs& a, int64_t t, bool real, int lane, int chosen, double w) {
@@ -323,11 +329,12 @@ __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(
 //   the sum with the bias u of it, and d u of that: 2 u of the largest.
 // so two experts whose d differ by more than 2 err and the nine bits are in
 // order.  Without a bias d comes from the logits themselves and never reverses
-// them: any two different keys are in order if the logits differ at all.  Two more experts than asked for are taken.  If neighbours among them are
-// not clear of one another, their 64-bit scores rank them; if the last one
-// chosen is not clear of the last one taken, somebody left out might belong in,
-// and the wave does the token in 64 bits.  So it does if groups are not clear
-// of one another or a lane's list ran out.
+// them: any two different keys are in order if the logits differ at all.  Two
+// more experts than asked for are taken.  If neighbours among them are not
+// clear of one another, their 64-bit scores rank them; if the last one chosen
+// is not clear of the last one taken, somebody left out might belong in, and
+// the wave does the token in 64 bits.  So it does if groups are not clear of
+// one another or a lane's list ran out.
 enum { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };  // what is chosen by: x, or the score with a bias
 template <int L, int P, int BY>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
@@ -523,73 +530,216 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
   }
 }
 
-// Gradient, one wave per token: with ds_e = d loss / d s_e,
+// ------------------------------------------------------------- gradient ---
+// With ds_e = d loss / d s_e,
 //   renormalised  ds_e = scale (dw_e - sum_k dw_k s_k / S) / S, S = sum of the chosen scores,
 //   else          ds_e = scale dw_e,
 // plus dscores; dx = ds s (1 - s), or s (ds - sum over all experts of ds s).
-__global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_kernel(GateBwdArgs a) {
-  const int lane = threadIdx.x & 63;
-  for (int t = (int)blockIdx.x * kGateWaves + (int)(threadIdx.x >> 6); t < a.tokens; t += (int)gridDim.x * kGateWaves) {
-    const int64_t row = (int64_t)t * a.ld;
-    auto logit = [&](int e) { return as_logit(ld_logit(a.logits, a.lf32, row + e)); };
+// Of the renormalised softmax that sum is 0: its weights are a softmax of the
+// chosen logits alone.  Every step is in 64 bits: what is left of a difference
+// may be little.
+
+// What lane j of a token's lanes knows of its j-th choice: the expert (-1:
+// none), the gradient of its weight (0 without one) and its logit.
+struct GateChoice {
+  int e;
+  double dw, x;
+};
+template <int L>
+__device__ __forceinline__ GateChoice gate_choice(const GateBwdArgs& a, int64_t t, int lane) {
+  GateChoice c{-1, 0.0, kNone};
+  if (lane < a.topk) {
+    const int64_t at = t * a.topk + lane;
+    const int64_t e = a.i64 ? static_cast<const int64_t*>(a.chosen)[at] : static_cast<const int32_t*>(a.chosen)[at];
+    if (e >= 0 && e < a.experts) {
+      c.e = (int)e;
+      c.dw = (double)a.dweights[at];
+      c.x = as_logit(ld_logit(a.logits, a.lf32, t * a.ld + e));
+    }
+  }
+  return c;
+}
+
+// v summed over the token's choices of the same expert, in their order; a
+// choice is nearly always alone with its expert.
+template <int L>
+__device__ __forceinline__ double gate_same(double v, int e, int topk) {
+  bool twice = false;
+  for (int j = 1; j < topk; ++j) {
+    const int other = __shfl_down(e, j, L);
+    twice = twice || (e >= 0 && other == e && (int)(threadIdx.x & (L - 1)) + j < L);
+  }
+  if (__builtin_amdgcn_ballot_w64(twice) == 0) return v;
+  double sum = 0.0;
+  for (int j = 0; j < topk; ++j) {
+    const int ej = __shfl(e, j, L);
+    const double vj = __shfl(v, j, L);
+    sum += ej == e ? vj : 0.0;
+  }
+  return sum;
+}
+
+// A sigmoid and its slope s (1 - s) = t / (1 + t)^2, t = e^-|x|.  1 + t is in
+// [1, 2]: its reciprocal needs no scaling, and two Newton steps after the
+// approximate one (half the cost of a division).
+struct Sigmoid {
+  double s, slope;
+};
+__device__ __forceinline__ Sigmoid sigmoid64(double x) {
+  const double t = exp64(-fabs(x)), d = 1.0 + t;
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return {x < 0.0 ? t * r : r, t * r * r};
+}
+
+// Where only the chosen experts have a gradient (a sigmoid, or the renormalised
+// softmax, without dscores): the row is laid out in LDS, zeros but for them, and
+// its logits are read at them alone.  L lanes a token.
+template <int L>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_few_kernel(GateBwdArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float rows[];
+  constexpr int kTokens = 64 / L;
+  const int lane = threadIdx.x & (L - 1), sub = (threadIdx.x & 63) / L;
+  const int pad = (a.experts + 7) / 8 * 8;
+  float* r = rows + ((threadIdx.x >> 6) * kTokens + sub) * pad;
+  const int64_t stride = (int64_t)gridDim.x * kGateWaves * kTokens;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kGateWaves + (int)(threadIdx.x >> 6)) * kTokens; t0 < a.tokens; t0 += stride) {
+    const bool real = t0 + sub < a.tokens;
+    const int64_t t = real ? t0 + sub : a.tokens - 1;
+    const GateChoice c = gate_choice<L>(a, t, lane);
+    for (int i = lane * 4; i < pad; i += L * 4) *reinterpret_cast<float4*>(r + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    gate_wave_fence();
+    double dx;
+    if (a.sigmoid) {
+      const Sigmoid y = sigmoid64(c.x);
+      double ds = c.dw;
+      if (a.renormalize) {
+        const double s = c.x > kNone ? y.s : 0.0;
+        const double total = gate_sum<L>(s), dot = gate_sum<L>(c.x > kNone ? c.dw * s : 0.0);
+        const double inv = total > 0.0 ? 1.0 / total : 0.0;
+        ds = (c.dw - dot * inv) * inv;
+      }
+      dx = a.scale * ds * y.slope;
+    } else {
+      const double top = gate_max<L>(c.x);
+      const double e = c.x > kNone ? exp64(c.x - top) : 0.0;
+      const double total = gate_sum<L>(e), w = total > 0.0 ? e / total : 0.0;
+      const double dot = gate_sum<L>(c.e >= 0 ? c.dw * w : 0.0);
+      dx = a.scale * w * (c.dw - dot);
+    }
+    dx = gate_same<L>(c.x > kNone ? dx : 0.0, c.e, a.topk);
+    if (c.e >= 0) r[c.e] = (float)dx;
+    gate_wave_fence();
+    if (!real) continue;
+    if (a.of32) {
+      for (int i = lane * 4; i < a.experts; i += L * 4) {
+        const float4 v = *reinterpret_cast<const float4*>(r + i);
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        st_float4(static_cast<float*>(a.dlogits) + t * a.ldd + i, f, a.experts - i, false);
+      }
+    } else {
+      for (int i = lane * 8; i < a.experts; i += L * 8) {
+        const float4 u = *reinterpret_cast<const float4*>(r + i), v = *reinterpret_cast<const float4*>(r + i + 4);
+        const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        st_bf16x8(static_cast<uint16_t*>(a.dlogits) + t * a.ldd + i, pack_bf16x8(f), a.experts - i, false);
+      }
+    }
+  }
+}
+
+// Every expert: a lane has P consecutive ones, the chosen ones' ds comes to it
+// through LDS, where the lanes' p-th values lie side by side.
+template <int L, int P>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_all_kernel(GateBwdArgs a) {
+  extern __shared__ __attribute__((aligned(16))) double ds_rows[];
+  constexpr int kTokens = 64 / L;
+  const int lane = threadIdx.x & (L - 1), sub = (threadIdx.x & 63) / L, base = lane * P;
+  double* r = ds_rows + ((threadIdx.x >> 6) * kTokens + sub) * (L * P);
+  const int64_t stride = (int64_t)gridDim.x * kGateWaves * kTokens;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kGateWaves + (int)(threadIdx.x >> 6)) * kTokens; t0 < a.tokens; t0 += stride) {
+    const bool real = t0 + sub < a.tokens;
+    const int64_t t = real ? t0 + sub : a.tokens - 1;
+    const GateChoice c = gate_choice<L>(a, t, lane);
+    float f[P], g[P];
+#pragma unroll
+    for (int p = 0; p < P; p += 4) {
+      const int left = a.experts - base - p;
+      if (a.lf32) {
+        const auto v = ld_raw<true, 4, true>(a.logits, t * a.ld + base + p, left, false);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[p + i] = v.at(i);
+      } else {
+        const auto v = ld_raw<false, 4, true>(a.logits, t * a.ld + base + p, left, false);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[p + i] = v.at(i);
+      }
+      const auto v = ld_raw<true, 4, true>(a.dscores, t * a.experts + base + p, a.dscores ? left : 0, false);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[p + i] = v.at(i);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) r[p * L + lane] = 0.0;
+    gate_wave_fence();
     double top = kNone, inv = 0.0;
-    if (!a.sigmoid) {
-      for (int e = lane; e < a.experts; e += 64) top = fmax(top, logit(e));
-      top = gate_max<64>(top);
+    double s[P];  // scores, or slopes of the sigmoid
+#pragma unroll
+    for (int p = 0; p < P; ++p) s[p] = base + p < a.experts ? as_logit(f[p]) : kNone;
+    if (a.sigmoid) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) s[p] = s[p] > kNone ? sigmoid64(s[p]).slope : 0.0;
+    } else {
+      top = gate_max<L>(gate_tree_max<P>(s));
       double total = 0.0;
-      for (int e = lane; e < a.experts; e += 64) {
-        const double x = logit(e);
-        if (x > kNone) total += exp64(x - top);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        s[p] = s[p] > kNone ? exp64(s[p] - top) : 0.0;
+        total += s[p];
       }
-      total = gate_sum<64>(total);
+      total = gate_sum<L>(total);
       inv = total > 0.0 ? 1.0 / total : 0.0;
+#pragma unroll
+      for (int p = 0; p < P; ++p) s[p] *= inv;
     }
-    // lane j: the j-th choice
-    int e = -1;
-    double ds = 0.0;
-    if (lane < a.topk) {
-      const int64_t at = (int64_t)t * a.topk + lane;
-      const int64_t c = a.i64 ? static_cast<const int64_t*>(a.chosen)[at] : static_cast<const int32_t*>(a.chosen)[at];
-      if (c >= 0 && c < a.experts) {
-        e = (int)c;
-        ds = (double)a.dweights[at];
-      }
-    }
+    const double mine = c.e >= 0 ? score_of(c.x, a.sigmoid, top, inv) : 0.0;
+    double ds = c.dw;
     if (a.renormalize) {
-      const double s = e >= 0 ? score_of(logit(e), a.sigmoid, top, inv) : 0.0;
-      const double total = gate_sum<64>(s), dot = gate_sum<64>(e >= 0 ? ds * s : 0.0);
-      ds = total > 0.0 ? (ds - dot / total) / total : 0.0;
+      const double total = gate_sum<L>(mine), dot = gate_sum<L>(c.e >= 0 ? c.dw * mine : 0.0);
+      ds = total > 0.0 ? (c.dw - dot / total) / total : 0.0;
     }
-    ds *= a.scale;
-    auto grad = [&](int i) {
-      double d = a.dscores ? (double)a.dscores[(int64_t)t * a.experts + i] : 0.0;
-      for (int j = 0; j < a.topk; ++j) {
-        const int ej = __shfl(e, j);
-        const double dj = __shfl(ds, j);
-        if (ej == i) d += dj;
-      }
-      return d;
-    };
+    ds = c.x > kNone ? a.scale * ds : 0.0;
     double mean = 0.0;
     if (!a.sigmoid) {
-      for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const int i = min(e0 + lane, a.experts - 1);
-        const double x = logit(i), d = grad(i) * score_of(x, false, top, inv);
-        if (e0 + lane < a.experts && x > kNone) mean += d;
-      }
-      mean = gate_sum<64>(mean);
+      mean = c.e >= 0 ? ds * mine : 0.0;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (s[p] > 0.0) mean += (double)g[p] * s[p];
+      mean = gate_sum<L>(mean);
     }
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-      const int i = min(e0 + lane, a.experts - 1);
-      const double x = logit(i), s = score_of(x, a.sigmoid, top, inv);
-      double d = a.sigmoid ? grad(i) * s * (1.0 / (1.0 + exp64(x))) : s * (grad(i) - mean);
-      if (!(x > kNone)) d = 0.0;
-      if (e0 + lane < a.experts) {
-        const int64_t at = (int64_t)t * a.ldd + i;
-        if (a.of32) {
-          static_cast<float*>(a.dlogits)[at] = (float)d;
+    ds = gate_same<L>(ds, c.e, a.topk);
+    if (c.e >= 0) r[c.e % P * L + c.e / P] = ds;
+    gate_wave_fence();
+    float d[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) d[p] = s[p] > 0.0 ? (float)((r[p * L + lane] + (double)g[p] - mean) * s[p]) : 0.0f;
+    gate_wave_fence();
+    if (!real) continue;
+#pragma unroll
+    for (int p = 0; p < P; p += 4) {
+      const int left = a.experts - base - p;
+      if (left <= 0) continue;
+      if (a.of32) {
+        st_float4(static_cast<float*>(a.dlogits) + t * a.ldd + base + p, d + p, left, false);
+      } else {
+        const uint32_t lo = __builtin_bit_cast(uint32_t, c8_v2bf{(__bf16)d[p], (__bf16)d[p + 1]});
+        const uint32_t hi = __builtin_bit_cast(uint32_t, c8_v2bf{(__bf16)d[p + 2], (__bf16)d[p + 3]});
+        uint16_t* o = static_cast<uint16_t*>(a.dlogits) + t * a.ldd + base + p;
+        if (left >= 4) {
+          *reinterpret_cast<Any8*>(o) = Any8{{lo, hi}};
         } else {
-          static_cast<uint16_t*>(a.dlogits)[at] = __builtin_bit_cast(uint16_t, (__bf16)(float)d);
+          o[0] = (uint16_t)lo;
+          if (left > 1) o[1] = (uint16_t)(lo >> 16);
+          if (left > 2) o[2] = (uint16_t)hi;
         }
       }
     }
@@ -655,8 +805,24 @@ hipError_t launch_gate(GateArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// 16 lanes a token leave a quarter of the waves, 64 the shorter way through a
+// row.  Gradients at the choice alone, eight of 256 (us, 16 lanes / 64): 3.2 /
+// 2.9 at one token, 3.8 / 3.8 at 2048, 4.1 / 4.6 at 4096, 8.5 / 12.0 at 16384.
+// At every expert (a sigmoid's with dscores): of 60, 3.6 / 3.6 at one token,
+// 6.4 / 16.5 at 16384; of 128, 5.3 / 5.0 at 2048, 5.5 / 6.5 at 4096, 11.7 /
+// 18.8 at 16384; of 256, 6.8 / 3.8 at one, 22.5 / 19.4 at 16384.
 hipError_t launch_gate_backward(const GateBwdArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(gate_bwd_kernel, dim3(gate_grid(a.tokens)), dim3(64 * kGateWaves), 0, stream, a);
+  const bool all = a.dscores || (!a.sigmoid && !a.renormalize);
+  const bool wide = a.topk > 16 || (all ? a.experts > (a.tokens >= 4096 ? 128 : 64) : a.tokens < 2048);
+  const int lanes = wide ? 64 : 16, tokens = kGateWaves * 64 / lanes;
+  const dim3 grid(gate_grid(((int64_t)a.tokens * lanes + 63) / 64)), block(64 * kGateWaves);
+  if (all) {
+    const bool four = a.experts <= 4 * lanes;
+    const auto kernel = wide ? (four ? gate_bwd_all_kernel<64, 4> : gate_bwd_all_kernel<64, 8>) : (four ? gate_bwd_all_kernel<16, 4> : gate_bwd_all_kernel<16, 8>);
+    hipLaunchKernelGGL(kernel, grid, block, (size_t)tokens * lanes * (four ? 4 : 8) * sizeof(double), stream, a);
+  } else {
+    hipLaunchKernelGGL(wide ? gate_bwd_few_kernel<64> : gate_bwd_few_kernel<16>, grid, block, (size_t)tokens * ((a.experts + 7) / 8 * 8) * sizeof(float), stream, a);
+  }
   return hipGetLastError();
 }
 

@@ -179,6 +179,27 @@ def test_route_backward(tokens, n, topk, score, renormalize, dtype, odt):
             assert (host(got.float())[~(x > -np.inf)] == 0).all()
 
 
+@pytest.mark.parametrize("n,topk", [(256, 8), (60, 4), (128, 16), (100, 3), (512, 17), (130, 5)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_route_backward_of_many_tokens(n, topk, score, renormalize):
+    """Batches in which several tokens share a wave: each token as it is alone."""
+    r = np.random.default_rng(n)
+    x = logits_of(r, 41, n, F32)
+    e, _, _ = B.route(x, topk)
+    e[0, 0], e[-1, 1], e[-1, 2] = n, e[-1, 0], -7
+    dw = r.normal(size=(41, topk)).astype(np.float32)
+    for dscores in (None, r.normal(size=(41, n)).astype(np.float32)):
+        want, mag = B.route_backward(dw, e, x, score, renormalize, 2.5, dscores)
+        # 64-bit steps of the magnitudes that are added, a hundred or so of them, and the rounding of the result
+        bound = 2.0 ** -24 * 1.01 * np.abs(want) + 200 * 2.0 ** -53 * mag + 2.0 ** -134
+        for tokens in (2050, MANY):
+            rows = np.arange(tokens) % 41
+            got = host(fp8q.moe_route_backward(dev(dw[rows]), dev(e[rows]), dev(x[rows]), score=score, renormalize=renormalize, scale=2.5,
+                                               dscores=None if dscores is None else dev(dscores[rows])).double())
+            assert (np.abs(got - want[rows]) <= bound[rows]).all(), (tokens, dscores is None)
+
+
 def test_route_backward_gap_and_strides():
     """Output rows of any stride, through the C ABI; nothing behind them is written."""
     r = np.random.default_rng(6)
