@@ -329,13 +329,18 @@ __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(
 //   the sum with the bias u of it, and d u of that: 2 u of the largest.
 // so two experts whose d differ by more than 2 err and the nine bits are in
 // order.  Without a bias d comes from the logits themselves and never reverses
-// them: any two different keys are in order if the logits differ at all.  Two
-// more experts than asked for are taken.  If neighbours among them are not
-// clear of one another, their 64-bit scores rank them; if the last one chosen
-// is not clear of the last one taken, somebody left out might belong in, and
-// the wave does the token in 64 bits.  So it does if groups are not clear of
-// one another or a lane's list ran out.
+// them: any two different keys are in order if the logits differ at all.  Nor
+// do BF16 logits x with |x| >= d / 32 share a d unless they are equal: others
+// lie 2^-8 |x| away or more, and the d of a key steps by 2^-14 d.
+// Two more experts than asked for are taken.  Where neighbours among them are
+// not clear of one another, they change places by their 64-bit scores; if the
+// last one chosen is not clear of the last one taken, somebody left out might
+// belong in, and the wave does the token in 64 bits.  So it does if groups are
+// not clear of one another or a lane's list ran out.
 enum { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };  // what is chosen by: x, or the score with a bias
+struct Four {
+  double a, b, c, d;
+};
 template <int L, int P, int BY>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
   constexpr int kTokens = 64 / L;         // of a wave
@@ -467,25 +472,29 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
     };
     // neighbours: lane j and j + 1
     const uint32_t next = (uint32_t)__shfl_down((int)cand, 1, L), last = (uint32_t)__shfl((int)cand, taken - 1, L);
-    const float logit_next = __shfl_down(logit, 1, L);
+    const float logit_next = __shfl_down(logit, 1, L), logit_last = __shfl(logit, taken - 1, L);
     bool close = lane < a.topk && next != kNoKey && !behind(cand, next);
     if (BY == kByLogit) close = close && logit != logit_next;  // (equal logits go by index)
     const uint64_t any_close = __builtin_amdgcn_ballot_w64(close);
     double s_top = kNone, s_inv = 0.0;
+    // (four experts at a time, from the cache: all side by side their steps would
+    // fill the registers of every call)
+    auto four = [&](int p0, auto f) {
+      double v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f(as_logit(ld_logit(a.logits, a.lf32, row + first + min(p0 + i, mine - 1))));
+      return Four{v[0], v[1], v[2], v[3]};
+    };
+    Four e{};  // the first four's exponentials
     if (!a.sigmoid) {
       // the 64-bit denominator where it is asked for
       s_top = as_logit(top);
       s_inv = 1.0;
-      if (!a.renormalize || a.scores || any_close) {
-        // (four experts at a time, from the cache: all side by side their steps would
-        // fill the registers of every call)
+      if (!a.renormalize || a.scores || (BY == kBySoftmax && any_close)) {
         double total = 0.0;
         for (int p0 = 0; p0 < mine; p0 += 4) {
-          double e[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = exp64(as_logit(ld_logit(a.logits, a.lf32, row + first + min(p0 + i, mine - 1))) - s_top);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) total += p0 + i < mine ? e[i] : 0.0;
+          e = four(p0, [&](double v) { return exp64(v - s_top); });
+          total += e.a + (p0 + 1 < mine ? e.b : 0.0) + ((p0 + 2 < mine ? e.c : 0.0) + (p0 + 3 < mine ? e.d : 0.0));
         }
         total = gate_sum<L>(total);
         s_inv = total > 0.0 ? 1.0 / total : 0.0;
@@ -494,32 +503,35 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
     if (a.scores && real) {
       float* out = a.scores + t * a.experts + first;
       for (int p0 = 0; p0 < mine; p0 += 4) {
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = score32(as_logit(ld_logit(a.logits, a.lf32, row + first + min(p0 + i, mine - 1))), a.sigmoid, s_top, s_inv);
+        if (P > 4 || a.sigmoid) e = four(p0, [&](double v) { return (double)score32(v, a.sigmoid, s_top, s_inv); });
+        const bool unscaled = P <= 4 && !a.sigmoid;
+        const float v[4] = {(float)(unscaled ? e.a * s_inv : e.a), (float)(unscaled ? e.b * s_inv : e.b), (float)(unscaled ? e.c * s_inv : e.c),
+                            (float)(unscaled ? e.d * s_inv : e.d)};
         st_float4(out + p0, v, mine - p0, false);
       }
     }
     double s = chosen >= 0 ? score_of(as_logit(logit), a.sigmoid, s_top, s_inv) : 0.0;
     if (any_close) {
-      // the taken ones in their 64-bit order
-      const double k = chosen < 0 ? kNone : BY == kByLogit ? as_logit(logit) : s + (double)a.bias[chosen];
-      int place = 0;
-      for (int j = 0; j < taken; ++j) {
-        const double kj = __shfl(k, j, L);
-        const int ej = __shfl(chosen, j, L);
-        place += kj > k || (kj == k && ej >= 0 && ej < chosen);
+      // the taken ones in their 64-bit order: neighbours change places until none are wrong
+      double k = chosen < 0 ? kNone : BY == kByLogit ? as_logit(logit) : s + (double)a.bias[chosen];
+      const int me = threadIdx.x & 63;
+      while (true) {
+        const double kn = __shfl_down(k, 1, L);
+        const int en = __shfl_down(chosen, 1, L);
+        const uint64_t wrong = __builtin_amdgcn_ballot_w64(lane + 1 < taken && (kn > k || (kn == k && en >= 0 && en < chosen)));
+        if (!wrong) break;
+        const uint64_t even = wrong & 0x5555555555555555ull, pick = even ? even : wrong;  // (the first of each pair)
+        const int from = lane + (int)(pick >> me & 1) - (int)(pick << 1 >> me & 1);
+        k = __shfl(k, from, L);
+        s = __shfl(s, from, L);
+        chosen = __shfl(chosen, from, L);
+        cand = (uint32_t)__shfl((int)cand, from, L);
       }
-      int from = lane;  // lane j takes the one whose place is j
-      for (int j = 0; j < taken; ++j) {
-        if (__shfl(place, j, L) == lane) from = j;
-      }
-      chosen = __shfl(chosen, from, L);
-      s = __shfl(s, from, L);
-      cand = (uint32_t)__shfl((int)cand, from, L);
     }
     // the chosen ones have to be clear of whatever was left out, all of it behind the last one taken
-    unsure = unsure || (lane < a.topk && cand != kNoKey && last != kNoKey && !behind(cand, last));
+    bool open_end = lane < a.topk && cand != kNoKey && last != kNoKey && !behind(cand, last);
+    if (BY == kByLogit && !a.lf32) open_end = open_end && !(fabsf(logit_last) >= __uint_as_float(last & ~511u) * 0x1p-5f);
+    unsure = unsure || open_end;
     const uint64_t redo = __builtin_amdgcn_ballot_w64(unsure);
     auto again = [&](int i) { return (redo >> (i * L & 63) & (~0ull >> (64 - L))) != 0; };  // token i of the wave
     gate_write<L>(a, t, real && !again(sub), lane, lane < a.topk ? chosen : -1, lane < a.topk ? s : 0.0);
@@ -771,10 +783,10 @@ static void launch_gate_lanes(const GateArgs& a, int per, hipStream_t stream) {
 }
 
 // Four tokens a wave take less time in all, one a wave less for each: of 256
-// experts, 2048 tokens 8.2 against 7.3 us, 4096 9.1 against 9.3, 16384 14.0
-// against 21.9; of 60, 1024 tokens 4.2 against 4.3, 16384 6.2 against 15.0.  The
+// experts, 2048 tokens 7.4 against 6.8 us, 4099 8.8 against 9.5, 16384 13.2
+// against 22.7; of 60, 1024 tokens 3.6 against 3.9, 16384 5.5 against 15.4.  The
 // scores of all experts, which are written in 64-bit steps, are many for a lane
-// of few: 4099 tokens of 160 14.3 against 12.0, 16384 24.9 against 29.0.
+// of few: 4099 tokens of 160 11.4 against 8.5, 16384 19.2 against 23.3.
 static int gate_narrow_from(const GateArgs& a) { return a.scores ? 16384 : a.narrow.per <= 8 ? 1024 : 4096; }
 
 // How `lanes` lanes a token share out the experts (GateLane).
