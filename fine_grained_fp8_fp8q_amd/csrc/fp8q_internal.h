@@ -210,13 +210,17 @@ struct NormBwdArgs {
   bool df32, hf32, wf32, of32, pow2;
 };
 // How the backward pass goes over its rows (rows, n > 0; f32: some tensor of
-// them is float32): a wave a row while `chunks` of eight columns a thread hold
-// it (0: the row is longer than that of 512 threads), a workgroup above;
+// them is float32): a wave a row while `chunks` of eight columns a lane hold
+// it, a workgroup above (chunks 0: the row is longer than that of 512 threads).
+// Three chunks of float32 values leave one wave a SIMD: only where there are
+// rows enough (8192 rows of 1030 35 us, 43 by workgroups of two chunks a
+// thread; 1001 13.2 and 12.8).
 // `blocks` workgroups (of longer rows: blocks of them), each with a share of
 // the gain's gradient.  As few blocks as keep the memory busy, since every
-// share is written and read again: 8192 rows of 7168 BF16 columns take 86 us
-// with 256 blocks, 90 with 512 (as many as fit), 94 with 1024; 4096 of 4096
-// 34.9, 33.4 and 37.1; 32768 of 512 34.5, 29.0 and 31.1.
+// share is written and read again: 8192 rows of 7168 BF16 columns take 87 us
+// with 256 blocks, 90 with 512 (as many as fit); 16384 of 2048 50 and 51; 8192
+// of 4096 62 and 56; 32768 of 512 34 and 28.  Few rows are spread over
+// workgroups of fewer waves (256 rows of 1030: 9.2 us, 10.6 in 64 of four).
 struct NormBwdShape {
   int threads, chunks, blocks;
   bool wave;
@@ -226,12 +230,13 @@ constexpr int kNormBwdBlocks = 512;
 inline NormBwdShape norm_bwd_shape(int rows, int n, bool f32) {
   const int items = (n + 7) / 8, most = f32 ? 2 : 4;
   NormBwdShape s{};
-  s.wave = items <= 64 * most;
-  s.chunks = n > kMaxNormRow / (f32 ? 2 : 1) ? 0 : items <= 64 ? 1 : items <= 128 ? 2 : most;
-  s.threads = s.wave ? 256 : s.chunks ? ((items + most - 1) / most + 63) / 64 * 64 : 1024;
-  const int64_t want = s.wave ? ((int64_t)rows + 3) / 4 : s.chunks ? rows : ((int64_t)rows + 31) / 32;
-  const int most_blocks = (s.wave ? s.chunks < 4 : s.threads < 256) || !s.chunks ? kNormBwdBlocks : kNormBwdBlocks / 2;
-  s.blocks = (int)(want < most_blocks ? want : most_blocks);
+  s.wave = items <= 64 * (most < 3 && rows >= 2048 ? 3 : most);
+  s.chunks = n > kMaxNormRow / (f32 ? 2 : 1) ? 0 : items <= 64 ? 1 : items <= 128 ? 2 : s.wave && items <= 192 ? 3 : most;
+  s.threads = s.chunks ? ((items + most - 1) / most + 63) / 64 * 64 : 1024;
+  const int blocks = (s.wave ? s.chunks < 4 : s.threads < 256) || !s.chunks ? kNormBwdBlocks : kNormBwdBlocks / 2;
+  if (s.wave) s.threads = 64 * (rows > 3 * blocks ? 4 : (rows + blocks - 1) / blocks);
+  const int64_t want = s.wave ? ((int64_t)rows * 64 + s.threads - 1) / s.threads : s.chunks ? rows : ((int64_t)rows + 31) / 32;
+  s.blocks = (int)(want < blocks ? want : blocks);
   return s;
 }
 // blocks of the workspace: no shape has more

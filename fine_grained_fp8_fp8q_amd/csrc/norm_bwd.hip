@@ -9,6 +9,7 @@
 namespace fp8q {
 namespace {
 
+constexpr int kSlots = 4;  // waves of a workgroup, each on a row of its own
 constexpr int kNormThreads = 256;
 constexpr int kMaxNormThreads = 1024;
 
@@ -30,7 +31,7 @@ struct NormBwdRow {
 template <bool DF32, bool HF32, bool OF32, bool VEC, bool KEEP, int CH, bool WAVE>
 __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_bwd_rows_kernel(NormBwdArgs a) {
   __shared__ double part[2][kMaxNormThreads / 64];
-  __shared__ float share[WAVE ? CH * 512 : 1];
+  __shared__ __attribute__((aligned(16))) float4 share[WAVE ? kSlots * CH * 128 : 1];
   const int slot = WAVE ? (int)threadIdx.x >> 6 : 0, tid = WAVE ? (int)threadIdx.x & 63 : (int)threadIdx.x;
   const int lanes = WAVE ? 64 : (int)blockDim.x, slots = WAVE ? (int)blockDim.x >> 6 : 1, step = lanes * 8;
   auto load = [&](int64_t row) {
@@ -121,21 +122,27 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_bwd_rows_kernel(NormBwd
   }
   if (!a.dweight) return;
   if constexpr (WAVE) {
-    // the slots' shares, one after another
-    for (int s = 0; s < slots; ++s) {
-      if (slot == s) {
+    if (slots > 1) {
+      // the slots' shares side by side, four columns a place, then summed in their order
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float* p = share + (c * 8 + i) * 64 + tid;
-            dw[c][i] = s ? *p + dw[c][i] : dw[c][i];
-            if (s < slots - 1) *p = dw[c][i];
-          }
-      }
+        for (int i = 0; i < 8; i += 4) share[slot * CH * 128 + (2 * c + i / 4) * 64 + tid] = make_float4(dw[c][i], dw[c][i + 1], dw[c][i + 2], dw[c][i + 3]);
       __syncthreads();
+      for (int k = threadIdx.x; k < CH * 128; k += blockDim.x) {
+        const int col = (k >> 7) * 512 + (k & 63) * 8;
+        float4 v = share[k];
+        for (int s = 1; s < slots; ++s) {
+          const float4 u = share[s * CH * 128 + k];
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        }
+        if (col < a.n) *reinterpret_cast<float4*>(a.partial + (int64_t)blockIdx.x * a.ldp + col + (k >> 6 & 1) * 4) = v;
+      }
+      return;
     }
-    if (slot < slots - 1) return;
   }
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -242,11 +249,12 @@ __global__ __launch_bounds__(1024) void norm_dw_sum_kernel(const float* partial,
 
 template <bool DF32, bool HF32, bool OF32, bool VEC, bool KEEP>
 static void launch_norm_bwd_rows(const NormBwdArgs& a, const NormBwdShape& s, hipStream_t stream) {
-  // (a row and the next one of float32 values take the registers at two chunks)
+  // (of a workgroup, a row and the next one of float32 values take the registers at two chunks)
   constexpr int kMost = DF32 || HF32 || OF32 ? 2 : 4;
   auto kernel = !s.wave         ? norm_bwd_rows_kernel<DF32, HF32, OF32, VEC, KEEP, kMost, false>
                 : s.chunks == 1 ? norm_bwd_rows_kernel<DF32, HF32, OF32, VEC, KEEP, 1, true>
                 : s.chunks == 2 ? norm_bwd_rows_kernel<DF32, HF32, OF32, VEC, KEEP, 2, true>
+                : s.chunks == 3 ? norm_bwd_rows_kernel<DF32, HF32, OF32, VEC, KEEP, 3, true>
                                 : norm_bwd_rows_kernel<DF32, HF32, OF32, VEC, KEEP, kMost, true>;
   hipLaunchKernelGGL(kernel, dim3(s.blocks), dim3(s.threads), 0, stream, a);
 }

@@ -249,7 +249,7 @@ __device__ __forceinline__ Raw<F32, 8> as_raw(const float* v) {
 template <bool POW2, bool VEC, int CH>
 __device__ __forceinline__ void encode_chunks(const uint4 (&d)[CH], uint32_t mine, int64_t row, int col0, int step, int n, uint8_t* codes,
                                               int64_t ldc, float* scales) {
-  static_assert(CH == 1 || CH == 2 || CH == 4, "tiles u = 0 .. CH - 1 of a DPP row");
+  static_assert(CH >= 1 && CH <= 4, "tiles u = 0 .. CH - 1 of a DPP row");
   const int sub = threadIdx.x & 15, nb = (n + 127) >> 7;
   const TileScale tm = tile_scale<POW2>(mine);
   {
@@ -273,10 +273,8 @@ __device__ __forceinline__ void encode_chunks(const uint4 (&d)[CH], uint32_t min
   auto all = [&](auto enc) {
     store(0, row_tile_scale<POW2, 0>(tm), enc);
     if constexpr (CH > 1) store(1, row_tile_scale<POW2, 1>(tm), enc);
-    if constexpr (CH > 2) {
-      store(2, row_tile_scale<POW2, 2>(tm), enc);
-      store(3, row_tile_scale<POW2, 3>(tm), enc);
-    }
+    if constexpr (CH > 2) store(2, row_tile_scale<POW2, 2>(tm), enc);
+    if constexpr (CH > 3) store(3, row_tile_scale<POW2, 3>(tm), enc);
   };
   if constexpr (POW2) {
     all([](uint4 x, const TileScale& t) { return encode8<true>(x, t); });

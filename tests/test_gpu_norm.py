@@ -242,6 +242,22 @@ def test_norm_backward_of_many_rows(rows, n):
     assert torch.equal(fp8q.rmsnorm_backward(*args)[3], dw)
 
 
+@pytest.mark.parametrize("n", [1030, 1500, 1536])
+@pytest.mark.parametrize("ddt,hdt,odt", [(F32, F32, F32), (F32, BF, F32), (BF, F32, BF), (BF, BF, BF)])
+def test_norm_backward_of_many_rows_of_three_chunks(n, ddt, hdt, odt):
+    rows = 2060
+    r = np.random.default_rng(n)
+    h, w, dy, res = rows_like(r, rows, n, hdt), values(r, (n,), BF), values(r, (rows, n), ddt), values(r, (rows, n), odt)
+    rstd = B.rms_reciprocal(h, EPS)
+    want = B.rmsnorm_backward(dy, h, rstd, w, res)
+    _, dw64, _, mag = B.rmsnorm_gradient(dy, h, rstd, w, res)
+    dx, codes, scales, dw = fp8q.rmsnorm_backward(on(dy, ddt), on(h, hdt), dev(rstd), dev(w).to(BF), dres=on(res, odt), out_dtype=odt, quantize=True)
+    same_f32(dx, B.round_to(want, "bf16" if odt == BF else "f32"), "dx")
+    same_rows((None, codes, scales), e4m3.f32_to_bf16_bits_rne(want), "free")
+    # one rounding of t, one a product or fused step, one an addition, in any order of the rows
+    assert (np.abs(host(dw.double()) - dw64) <= (rows + 2) * 2.0 ** -24 * mag * 1.01).all()
+
+
 def test_norm_backward_in_place_and_strides():
     """dx over the gradient it adds to, and output strides through the C ABI."""
     r = np.random.default_rng(8)
