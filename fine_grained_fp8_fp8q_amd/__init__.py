@@ -874,15 +874,13 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, out_dtype=None, quantize=Fa
         codes, ldc = _new_codes(rows, n, dev)
         scales = _new(rows, (n + 127) // 128, f32, dev)
     if want_dweight:
-        # one allocation: [dweight | workspace]
+        # (two allocations: a gradient that is kept should not keep the workspace)
+        dw = torch.empty_strided((n,), (1,), dtype=f32, device=dev)
         need = (_lib or load_library()).fp8q_rmsnorm_backward_workspace(rows, n)
-        pad = (n + 3) // 4 * 4
-        work = torch.empty_strided((pad + need // 4,), (1,), dtype=f32, device=dev)
-        dw = work.as_strided((n,), (1,))
-    at = _addr(dw)
+        work = torch.empty_strided((need // 4,), (1,), dtype=f32, device=dev)
     _call(dev, "fp8q_rmsnorm_backward", dy_p, types.index(dy.dtype), rows, n, ldd, h_p, types.index(h.dtype), ldh, rstd_p, w_p,
           types.index(weight.dtype), res_p, ldr, _addr(dx), types.index(out_dtype), n, _scale_mode(scale_mode), _addr(codes), ldc,
-          _addr(scales), at, at + 4 * pad if need else None, need)
+          _addr(scales), _addr(dw), _addr(work), need)
     return dx, codes, scales, dw
 
 

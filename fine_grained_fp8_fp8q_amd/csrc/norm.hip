@@ -27,12 +27,12 @@ __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) vo
   __shared__ double part[kMaxNormThreads / 64];
   const int tid = threadIdx.x, step = (int)blockDim.x * 8;
   const bool out = a.y || a.codes;
-  for (int row = blockIdx.x; row < a.rows; row += (int)gridDim.x) {
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     Raw<HF32, 8> h[CH];
     Gain8 w[CH];
     {
-      const Row<XF32, VEC, KEEP> rx(a.x, (int64_t)row * a.ldx, a.n);
-      const Row<HF32, VEC, KEEP> rs(RES ? a.res : a.x, RES ? (int64_t)row * a.ldr : 0, a.n);
+      const Row<XF32, VEC, KEEP> rx(a.x, row * a.ldx, a.n);
+      const Row<HF32, VEC, KEEP> rs(RES ? a.res : a.x, RES ? row * a.ldr : 0, a.n);
       Raw<XF32, 8> x[CH];
       Raw<HF32, 8> s[CH];
 #pragma unroll
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) vo
         }
       }
     }
-    const Row<HF32, VEC> rh(a.h, (int64_t)row * a.ldh, a.n);
+    const Row<HF32, VEC> rh(a.h, row * a.ldh, a.n);
     double sum = 0.0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) vo
     const float r = reciprocal_rms(block_sum(sum, part), a.inv_n, a.eps);
     if (tid == 0 && a.rstd) a.rstd[row] = r;
     if (out) {
-      const Row<false, VEC> ry(a.y, (int64_t)row * a.ldy, a.n);
+      const Row<false, VEC> ry(a.y, row * a.ldy, a.n);
       uint4 d[CH];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -100,10 +100,10 @@ __global__ __launch_bounds__(kMaxNormThreads) void norm_long_kernel(NormArgs a) 
   constexpr bool RES = STREAM != kNoStream, HF32 = RES ? STREAM == kStreamF32 : XF32;
   __shared__ double part[kMaxNormThreads / 64];
   const int tid = threadIdx.x, step = (int)blockDim.x * 8;
-  auto load = [&](int row, int col) {
-    const auto x = Row<XF32, false>(a.x, (int64_t)row * a.ldx, a.n).settled(col);
+  auto load = [&](int64_t row, int col) {
+    const auto x = Row<XF32, false>(a.x, row * a.ldx, a.n).settled(col);
     if constexpr (RES) {
-      const auto s = Row<HF32, false>(a.res, (int64_t)row * a.ldr, a.n).settled(col);
+      const auto s = Row<HF32, false>(a.res, row * a.ldr, a.n).settled(col);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = x.at(i) + s.at(i);
@@ -112,7 +112,7 @@ __global__ __launch_bounds__(kMaxNormThreads) void norm_long_kernel(NormArgs a) 
       return x;
     }
   };
-  for (int row = blockIdx.x; row < a.rows; row += (int)gridDim.x) {
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     double sum = 0.0;
     for (int col = tid * 8; col < a.n; col += step) {
       const auto h = load(row, col);
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kMaxNormThreads) void norm_long_kernel(NormArgs a) 
         const double v = (double)h.at(i);
         sum = __builtin_fma(v, v, sum);
       }
-      if (RES && a.h) Row<HF32, false>(a.h, (int64_t)row * a.ldh, a.n).store(col, h);
+      if (RES && a.h) Row<HF32, false>(a.h, row * a.ldh, a.n).store(col, h);
     }
     const float r = reciprocal_rms(block_sum(sum, part), a.inv_n, a.eps);
     if (tid == 0 && a.rstd) a.rstd[row] = r;
@@ -131,13 +131,13 @@ __global__ __launch_bounds__(kMaxNormThreads) void norm_long_kernel(NormArgs a) 
         Raw<HF32, 8> h = {};
         float w[8] = {}, v[8];
         if (col < a.n) {
-          h = RES && a.h ? Row<HF32, false>(a.h, (int64_t)row * a.ldh, a.n).settled(col) : load(row, col);
+          h = RES && a.h ? Row<HF32, false>(a.h, row * a.ldh, a.n).settled(col) : load(row, col);
           widen_gain8<false>(ld_gain8<false>(a.weight, a.wf32, col, a.n), a.wf32, col, a.n, w);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = normalised(h.at(i), r, w[i]);
         const uint4 d[1] = {pack_bf16x8(v)};
-        if (a.y) Row<false, false>(a.y, (int64_t)row * a.ldy, a.n).store(col, as_raw<false>(v));
+        if (a.y) Row<false, false>(a.y, row * a.ldy, a.n).store(col, as_raw<false>(v));
         if (a.codes) quantize_chunks<false, 1>(d, a.pow2, row, col, 0, a.n, a.codes, a.ldc, a.scales);
       }
     }

@@ -162,12 +162,12 @@ template <bool DF32, bool HF32, bool OF32>
 __global__ __launch_bounds__(kMaxNormThreads) void norm_bwd_long_kernel(NormBwdArgs a) {
   __shared__ double part[kMaxNormThreads / 64];
   const int step = (int)blockDim.x * 8, tid = threadIdx.x;
-  for (int row = blockIdx.x; row < a.rows; row += (int)gridDim.x) {
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float r = a.rstd[row];
     auto load = [&](int col, float* g, float* h) {
       float w[8];
-      widen(Row<DF32, false>(a.dy, (int64_t)row * a.lddy, a.n).settled(col), g);
-      widen(Row<HF32, false>(a.h, (int64_t)row * a.ldh, a.n).settled(col), h);
+      widen(Row<DF32, false>(a.dy, row * a.lddy, a.n).settled(col), g);
+      widen(Row<HF32, false>(a.h, row * a.ldh, a.n).settled(col), h);
       widen_gain8<false>(ld_gain8<false>(a.weight, a.wf32, col, a.n), a.wf32, col, a.n, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] *= w[i];
@@ -185,14 +185,14 @@ __global__ __launch_bounds__(kMaxNormThreads) void norm_bwd_long_kernel(NormBwdA
       float g[8] = {}, h[8] = {}, s[8] = {};
       if (left > 0) {
         load(col, g, h);
-        if (a.dres) widen(Row<OF32, false>(a.dres, (int64_t)row * a.lddr, a.n).settled(col), s);
+        if (a.dres) widen(Row<OF32, false>(a.dres, row * a.lddr, a.n).settled(col), s);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         g[i] = (g[i] - (h[i] * r) * mean) * r;
         if (a.dres) g[i] += s[i];
       }
-      if (a.dx) Row<OF32, false>(a.dx, (int64_t)row * a.lddx, a.n).store(col, as_raw<OF32>(g));
+      if (a.dx) Row<OF32, false>(a.dx, row * a.lddx, a.n).store(col, as_raw<OF32>(g));
       const uint4 d[1] = {pack_bf16x8(g)};
       if (a.codes) quantize_chunks<false, 1>(d, a.pow2, row, col, 0, a.n, a.codes, a.ldc, a.scales);
     }

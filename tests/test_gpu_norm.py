@@ -242,6 +242,14 @@ def test_norm_backward_of_many_rows(rows, n):
     assert torch.equal(fp8q.rmsnorm_backward(*args)[3], dw)
 
 
+def test_norm_gradients_hold_their_own_memory():
+    """What a caller keeps of the gradients holds no scratch memory."""
+    x, w, rstd = torch.randn(600, 1030, device="cuda:0").to(BF), torch.ones(1030, device="cuda:0"), torch.ones(600, device="cuda:0")
+    dx, codes, scales, dw = fp8q.rmsnorm_backward(x, x, rstd, w, quantize=True)
+    for t, most in ((dx, 600 * 1030 * 2), (codes, 600 * 1040), (scales, 600 * 9 * 4), (dw, 1030 * 4)):
+        assert t.untyped_storage().nbytes() <= most
+
+
 @pytest.mark.parametrize("n", [1030, 1500, 1536])
 @pytest.mark.parametrize("ddt,hdt,odt", [(F32, F32, F32), (F32, BF, F32), (BF, F32, BF), (BF, BF, BF)])
 def test_norm_backward_of_many_rows_of_three_chunks(n, ddt, hdt, odt):
