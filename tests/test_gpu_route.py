@@ -149,6 +149,20 @@ def test_route_large_and_empty():
     assert np.array_equal(host(e[pick]), we)
 
 
+@pytest.mark.parametrize("tokens,n,topk", [(1, 256, 8), (511, 256, 8), (512, 256, 8), (1025, 512, 4), (1024, 8, 8), (3001, 60, 3), (4100, 1, 1), (70, 512, 64)])
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_route_counts_its_pairs(tokens, n, topk, index):
+    r = np.random.default_rng(tokens)
+    x = logits_of(r, tokens, n, F32, True)
+    x[tokens // 2] = -np.inf  # padding, and what is added to
+    start = r.integers(0, 1000, size=n).astype(np.int32)
+    for bias in (None, np.where(np.arange(n) < 2, 9.0, 0.0).astype(np.float32)):
+        load = dev(start)
+        e, _, _ = fp8q.moe_route(dev(x), topk, bias=None if bias is None else dev(bias), index_dtype=index, load=load)
+        e = host(e).reshape(-1)
+        assert (e == -1).any() and np.array_equal(host(load), start + np.bincount(e[e >= 0], minlength=n))
+
+
 # -------------------------------------------------------------- backward ----
 
 @pytest.mark.parametrize("tokens,n,topk", [(1, 1, 1), (1, 256, 8), (5, 8, 8), (33, 60, 4), (70, 256, 8), (9, 160, 6), (3, 512, 64), (40, 65, 3), (6, 20, 0)])
