@@ -219,7 +219,8 @@ struct NormBwdArgs {
 // the gain's gradient.  As few blocks as keep the memory busy, since every
 // share is written and read again: 8192 rows of 7168 BF16 columns take 87 us
 // with 256 blocks, 90 with 512 (as many as fit); 16384 of 2048 50 and 51; 8192
-// of 4096 62 and 56; 32768 of 512 34 and 28.  Few rows are spread over
+// of 4096 62 and 56; 32768 of 512 34 and 28; and 4096 of 7001, whose rows begin
+// anywhere and take more instructions, 80 and 71.  Few rows are spread over
 // workgroups of fewer waves (256 rows of 1030: 9.2 us, 10.6 in 64 of four).
 struct NormBwdShape {
   int threads, chunks, blocks;
@@ -233,7 +234,7 @@ inline NormBwdShape norm_bwd_shape(int rows, int n, bool f32) {
   s.wave = items <= 64 * (most < 3 && rows >= 2048 ? 3 : most);
   s.chunks = n > kMaxNormRow / (f32 ? 2 : 1) ? 0 : items <= 64 ? 1 : items <= 128 ? 2 : s.wave && items <= 192 ? 3 : most;
   s.threads = s.chunks ? ((items + most - 1) / most + 63) / 64 * 64 : 1024;
-  const int blocks = (s.wave ? s.chunks < 4 : s.threads < 256) || !s.chunks ? kNormBwdBlocks : kNormBwdBlocks / 2;
+  const int blocks = (s.wave ? s.chunks < 4 : s.threads < 256 || n % 8) || !s.chunks ? kNormBwdBlocks : kNormBwdBlocks / 2;
   if (s.wave) s.threads = 64 * (rows > 3 * blocks ? 4 : (rows + blocks - 1) / blocks);
   const int64_t want = s.wave ? ((int64_t)rows * 64 + s.threads - 1) / s.threads : s.chunks ? rows : ((int64_t)rows + 31) / 32;
   s.blocks = (int)(want < blocks ? want : blocks);
