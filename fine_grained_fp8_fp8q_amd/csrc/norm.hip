@@ -1,13 +1,9 @@
-// Residual addition, RMS norm and 1x128 quantization in one pass, and the
-// norm's gradient, gfx950.
+// Residual addition, RMS norm and 1x128 quantization in one pass, gfx950.
 //
-// Forward, per row of n columns (norm_common.h has the roundings):
+// Per row of n columns (norm_common.h has the roundings):
 //   h = rn(x + res),  r = rn32(1 / sqrt(mean(h^2) + eps)),  y = bf16((h r) w),
 // y in BF16 and / or as E4M3 codes with 1x128 scales, what the quantizer would
 // make of that BF16 tensor.
-//
-// Backward, with g = dy w, c = rn32(mean(g h) r) (the sum in 64 bits):
-//   dx = (g - (h r) c) r + dres,   dw = sum over rows of dy (h r).
 #include "fp8q_internal.h"
 #include "norm_common.h"
 
@@ -17,9 +13,13 @@ namespace {
 constexpr int kMaxNormThreads = 1024;
 enum { kNoStream = 0, kStreamBF16 = 1, kStreamF32 = 2 };
 
-// -------------------------------------------------------------- forward ---
-// One workgroup per row, CH chunks of eight columns a thread, the row kept in
-// registers: every byte is moved once.
+// One workgroup per row, CH chunks of eight columns a thread (norm_chunks), the
+// row kept in registers: every byte is moved once.  With a residual HBM bounds
+// it: 16384 x 7168 BF16 to E4M3 137-139 us, 6.0 TB/s at 4:3 reads to writes (127 us
+// at the rates of plain reads and fills).  Without one the vector instructions
+// do, 20 a value: 82 us, where the bytes take 55; BF16 out 80, the bytes 73.
+// One row takes 3.6 us, 2.6 of them the launch: of the rest most is two loads
+// and a barrier in a row, one after another.
 template <bool XF32, int STREAM, bool VEC, bool KEEP, int CH>
 __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) void norm_row_kernel(NormArgs a) {
   static_assert(VEC || KEEP, "loads of unaligned rows are plain ones");
@@ -94,7 +94,9 @@ __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) vo
 
 // Rows of more columns than a workgroup's registers hold: the row is read
 // twice, the second time from the stream just written (which may be the
-// residual itself) where there is one.
+// residual itself) where there is one.  (512 x 20000 23 us, the bytes 11; the
+// second reading comes from the caches, but a workgroup's loads wait for one
+// another: 512 x 16384 in registers 14 us, the bytes 9.)
 template <bool XF32, int STREAM>
 __global__ __launch_bounds__(kMaxNormThreads) void norm_long_kernel(NormArgs a) {
   constexpr bool RES = STREAM != kNoStream, HF32 = RES ? STREAM == kStreamF32 : XF32;

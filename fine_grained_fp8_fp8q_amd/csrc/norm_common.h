@@ -7,7 +7,8 @@
 // y, of its codes and of its scales, is the same whichever way the row is
 // split over threads, in the forward pass and wherever y is formed again.  (A
 // float32 sum moves r by a step now and then, and with it a tile's scale by a
-// step of BF16.)  The 64-bit additions are hidden behind the row's loads.
+// step of BF16.)  The 64-bit steps are two of
+// some twenty instructions a value.
 #pragma once
 
 #include "chunk8.h"
