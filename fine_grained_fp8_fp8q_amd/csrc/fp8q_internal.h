@@ -284,8 +284,8 @@ struct GateArgs {
   int* load;      // null: not counted
   double scale;
   int tokens, experts, topk, groups, top_groups;
-  int per_group;           // (set by the launcher, as the splits
-  GateSplit wide, narrow;  // of 64 and 16 lanes a token)
+  int per_group;                   // (set by the launcher, as the splits
+  GateSplit wide, middle, narrow;  // of 64, 32 and 16 lanes a token)
   bool lf32, i64, sigmoid, two_best, renormalize;
 };
 hipError_t launch_gate(GateArgs a, hipStream_t stream);

@@ -51,14 +51,15 @@ __device__ __forceinline__ double gate_lane(double v, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// f over a token's L lanes (16: one DPP row, or the whole wave), the same in
-// each.  All 64 lanes must be active.
+// f over a token's L lanes (16: one DPP row, 32: two, or the whole wave), the
+// same in each.  All 64 lanes must be active.
 template <int L, class F>
 __device__ __forceinline__ double gate_all(double v, F f) {
   v = f(v, gate_dpp<0xB1>(v));
   v = f(v, gate_dpp<0x4E>(v));
   v = f(v, gate_dpp<0x141>(v));
   v = f(v, gate_dpp<0x140>(v));
+  if constexpr (L == 32) v = f(v, __shfl_xor(v, 16));
   if constexpr (L == 64) v = f(f(gate_lane(v, 0), gate_lane(v, 16)), f(gate_lane(v, 32), gate_lane(v, 48)));
   return v;
 }
@@ -123,7 +124,7 @@ struct GateLane {
   int lane, lpg, group, base, mine;  // lpg: lanes of a group; base, mine: the lane's first expert and their number
   bool fours;                        // groups of whole fours
   __device__ __forceinline__ explicit GateLane(const GateArgs& a) {
-    const GateSplit& s = L == 64 ? a.wide : a.narrow;
+    const GateSplit& s = L == 64 ? a.wide : L == 32 ? a.middle : a.narrow;
     lane = threadIdx.x & (L - 1);
     lpg = 1 << s.lane_bits;
     const int first = (lane & (lpg - 1)) * s.per;
@@ -298,6 +299,7 @@ __device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) { r
 template <int L>
 __device__ __forceinline__ uint32_t gate_max_u32(uint32_t v) {
   v = dpp_max16(v);
+  if constexpr (L == 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
   if constexpr (L == 64) {
     v = max(max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
             max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
@@ -352,7 +354,7 @@ template <int L, int P, int BY>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
   constexpr int kTokens = 64 / L;         // of a wave
   constexpr int T = P < 8 ? P : 8;        // experts in a lane's list
-  constexpr int kExactP = L == 64 ? P : 4;  // a quarter of P where four times the lanes share a token
+  constexpr int kExactP = P * L > 256 ? P * L / 64 : 4;  // fewer where all 64 lanes share a token
   constexpr float U = 0x1p-24f, kLow = -__builtin_inff(), kLog2e = 1.44269504f;
   constexpr uint32_t kNoKey = 0xFFFFFFFFu;
   const GateLane<L, P> at(a);
@@ -806,7 +808,9 @@ int gate_grid(int64_t waves) {
 
 template <int L, int BY>
 static void launch_gate_by(const GateArgs& a, int per, hipStream_t stream) {
-  auto kernel = per <= 4 ? gate_kernel<L, 4, BY> : per <= 8 ? gate_kernel<L, 8, BY> : gate_kernel<L, kGateLane, BY>;
+  // (of 32 lanes each has more than eight, or 16 would do)
+  auto kernel = L == 32 ? gate_kernel<L, kGateLane, BY> : per <= 4 ? gate_kernel<L, L == 32 ? kGateLane : 4, BY>
+                : per <= 8 ? gate_kernel<L, L == 32 ? kGateLane : 8, BY> : gate_kernel<L, kGateLane, BY>;
   const int64_t waves = ((int64_t)a.tokens * L + 63) / 64;
   hipLaunchKernelGGL(kernel, dim3(gate_grid(waves)), dim3(64 * kGateWaves), 0, stream, a);
 }
@@ -826,6 +830,9 @@ static void launch_gate_lanes(const GateArgs& a, int per, hipStream_t stream) {
 // against 22.7; of 60, 1024 tokens 3.6 against 3.9, 16384 5.5 against 15.4.  The
 // scores of all experts, which are written in 64-bit steps, are many for a lane
 // of few: 4099 tokens of 160 11.4 against 8.5, 16384 19.2 against 23.3.
+// Two tokens a wave, where four would leave a lane more experts than its
+// registers hold: of 384 experts, 2048 tokens 7.1 against 6.6 with one, 4096 7.9
+// against 8.2, 16384 18.0 against 23.1; of 512, sixteen of them, 24 against 31.
 static int gate_narrow_from(const GateArgs& a) { return a.scores ? 16384 : a.narrow.per <= 8 ? 1024 : 4096; }
 
 // How `lanes` lanes a token share out the experts (GateLane).
@@ -847,6 +854,7 @@ hipError_t launch_gate(GateArgs a, hipStream_t stream) {
   if (apart) a.load = nullptr;
   a.per_group = a.experts / a.groups;
   a.wide = gate_split(a, 64);
+  a.middle = gate_split(a, 32);
   a.narrow = gate_split(a, 16);
   if (a.topk + 2 > 64 || (a.groups > 1 && a.two_best && !a.bias)) {
     // (no lane for each expert taken, two more than asked for; groups by scores, experts by logits)
@@ -854,6 +862,8 @@ hipError_t launch_gate(GateArgs a, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(gate_grid(a.tokens)), dim3(64 * kGateWaves), 0, stream, a);
   } else if (a.narrow.fits && a.topk + 2 <= 16 && a.tokens >= gate_narrow_from(a)) {
     launch_gate_lanes<16>(a, a.narrow.per, stream);
+  } else if (!a.narrow.fits && a.middle.fits && a.topk + 2 <= 32 && a.tokens >= 4096) {
+    launch_gate_lanes<32>(a, a.middle.per, stream);
   } else {
     launch_gate_lanes<64>(a, a.wide.per, stream);
   }
