@@ -10,7 +10,7 @@
 // rounded.
 //
 // The batch of 16384 tokens, eight of 256 experts in four of eight groups, takes
-// 13.2 us (the bytes 2.8, the launch 2.6): 1180 vector instructions for the four
+// 13.6 us (the bytes 2.8, the launch 2.6): 1200 vector instructions for the four
 // tokens of a wave, all of whose 4096 start, load and choose at the same time.
 // One token takes 4.5 us.
 //
@@ -117,20 +117,27 @@ __device__ __forceinline__ float score32(double x, bool sigmoid, double top, dou
 }
 
 // The lanes of a token, L of them, are shared out evenly over the groups (L /
-// the power of two above them each); a lane holds up to P consecutive experts
-// of its group, by fours, so a lower lane's experts come before a higher one's.
-template <int L, int P>
+// the power of two above them each); a lane holds up to P experts of its group,
+// by fours.  Its fours are consecutive, so that a lower lane's experts come
+// before a higher one's, or (SPREAD) one of every round over the group's lanes:
+// loads of whole lines, and no lane with a list too short for neighbours that
+// are all among the best (16384 x 256 with the eight best side by side: 48 us
+// with consecutive fours, 13.9 so; 13.2 and 13.6 without such neighbours).
+template <int L, int P, bool SPREAD>
 struct GateLane {
-  int lane, lpg, group, base, mine;  // lpg: lanes of a group; base, mine: the lane's first expert and their number
-  bool fours;                        // groups of whole fours
+  int lane, lpg, group, base, step, mine;  // lpg: lanes of a group; base: the lane's first expert; step: from four to four
+  bool fours;                              // groups of whole fours
+  // The lane has the expert base + at(p) if at(p) < mine.
+  __device__ __forceinline__ int at(int p) const { return (p >> 2) * step + (p & 3); }
   __device__ __forceinline__ explicit GateLane(const GateArgs& a) {
     const GateSplit& s = L == 64 ? a.wide : L == 32 ? a.middle : a.narrow;
     lane = threadIdx.x & (L - 1);
     lpg = 1 << s.lane_bits;
-    const int first = (lane & (lpg - 1)) * s.per;
+    const int first = (lane & (lpg - 1)) * (SPREAD ? 4 : s.per);
+    step = SPREAD ? 4 * lpg : 4;
     group = lane >> s.lane_bits;
     base = group * a.per_group + first;
-    mine = group < a.groups ? min(max(a.per_group - first, 0), s.per) : 0;
+    mine = group < a.groups ? SPREAD ? a.per_group - first : min(max(a.per_group - first, 0), s.per) : 0;
     fours = a.per_group % 4 == 0;
   }
   // The lane's values of a row; those it does not have are the row's last.
@@ -139,18 +146,18 @@ struct GateLane {
     asm volatile("" : "+v"(base));  // (or an offset for every value is kept from turn to turn)
     if (!fours) {
 #pragma unroll
-      for (int c = 0; c < P; ++c) f[c] = ld_logit(p, f32, row + min(base + c, experts - 1));
+      for (int c = 0; c < P; ++c) f[c] = ld_logit(p, f32, row + min(base + at(c), experts - 1));
     } else if (f32) {
 #pragma unroll
       for (int c = 0; c < P; c += 4) {
-        const auto r = ld_raw<true, 4, true>(p, row + min(base + c, experts - 4), 4, false);
+        const auto r = ld_raw<true, 4, true>(p, row + min(base + at(c), experts - 4), 4, false);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[c + i] = r.at(i);
       }
     } else {
 #pragma unroll
       for (int c = 0; c < P; c += 4) {
-        const auto r = ld_raw<false, 4, true>(p, row + min(base + c, experts - 4), 4, false);
+        const auto r = ld_raw<false, 4, true>(p, row + min(base + at(c), experts - 4), 4, false);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[c + i] = r.at(i);
       }
@@ -200,7 +207,7 @@ __device__ __forceinline__ void gate_write(const GateArgs& a, int64_t t, bool re
 // One token by a whole wave, every step in 64 bits.
 template <int P>
 __device__ __forceinline__ void gate_exact(const GateArgs& a, int64_t t) {
-  const GateLane<64, P> at(a);
+  const GateLane<64, P, false> at(a);
   const int64_t row = t * a.ld;
   float f[P];
   at.load(a.logits, a.lf32, row, a.experts, f);
@@ -357,7 +364,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
   constexpr int kExactP = P * L > 256 ? P * L / 64 : 4;  // fewer where all 64 lanes share a token
   constexpr float U = 0x1p-24f, kLow = -__builtin_inff(), kLog2e = 1.44269504f;
   constexpr uint32_t kNoKey = 0xFFFFFFFFu;
-  const GateLane<L, P> at(a);
+  const GateLane<L, P, true> at(a);
   const int lane = at.lane, sub = (threadIdx.x & 63) / L, taken = a.topk + 2;
   const int64_t stride = (int64_t)gridDim.x * kGateWaves * kTokens;
   // (whole waves go round together; a token past the last is worked on as the last)
@@ -371,7 +378,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
     int mine = at.mine;
     asm volatile("" : "+v"(mine));  // (or a mask for every p is kept from turn to turn)
 #pragma unroll
-    for (int p = 0; p < P; ++p) x[p] = ((p < mine) & (x[p] == x[p])) ? fminf(x[p], 3.402823466e38f) : kLow;
+    for (int p = 0; p < P; ++p) x[p] = ((at.at(p) < mine) & (x[p] == x[p])) ? fminf(x[p], 3.402823466e38f) : kLow;
     float top = kLow, err = 0.0f;
     if (BY == kBySoftmax || !a.sigmoid) {
       top = gate_tree<P>(x, [](float u, float v) { return fmaxf(u, v); });
@@ -449,7 +456,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
     asm volatile("" : "+v"(first));
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t d = (__float_as_uint(high - key[p]) & ~511u) | (uint32_t)(first + p);
+      const uint32_t d = (__float_as_uint(high - key[p]) & ~511u) | (uint32_t)(first + at.at(p));
       const uint32_t k = key[p] > kLow ? d : kNoKey;
 #pragma unroll
       for (int i = T - 1; i > 0; --i)
@@ -468,7 +475,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
       m[T - 1] |= won;
       popped -= (int)won;
     }
-    if (P > T) unsure = unsure || (popped >= T && at.mine > T);
+    if (P > T) unsure = unsure || popped >= T;
     int chosen = cand != kNoKey ? (int)(cand & 511u) : -1;
     float logit = 0.0f;
     if (chosen >= 0) logit = ld_logit(a.logits, a.lf32, row + chosen);
@@ -488,10 +495,10 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
     double s_top = kNone, s_inv = 0.0;
     // (four experts at a time, from the cache: all side by side their steps would
     // fill the registers of every call)
-    auto four = [&](int p0, auto f) {
+    auto four = [&](int from, auto f) {  // those from base + from
       double v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = f(as_logit(ld_logit(a.logits, a.lf32, row + first + min(p0 + i, mine - 1))));
+      for (int i = 0; i < 4; ++i) v[i] = f(as_logit(ld_logit(a.logits, a.lf32, row + first + min(from + i, mine - 1))));
       return Four{v[0], v[1], v[2], v[3]};
     };
     Four e{};  // the first four's exponentials
@@ -501,9 +508,9 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
       s_inv = 1.0;
       if (!a.renormalize || a.scores || (BY == kBySoftmax && any_close)) {
         double total = 0.0;
-        for (int p0 = 0; p0 < mine; p0 += 4) {
-          e = four(p0, [&](double v) { return exp64(v - s_top); });
-          total += e.a + (p0 + 1 < mine ? e.b : 0.0) + ((p0 + 2 < mine ? e.c : 0.0) + (p0 + 3 < mine ? e.d : 0.0));
+        for (int from = 0; from < mine; from += at.step) {
+          e = four(from, [&](double v) { return exp64(v - s_top); });
+          total += e.a + (from + 1 < mine ? e.b : 0.0) + ((from + 2 < mine ? e.c : 0.0) + (from + 3 < mine ? e.d : 0.0));
         }
         total = gate_sum<L>(total);
         s_inv = total > 0.0 ? 1.0 / total : 0.0;
@@ -511,12 +518,12 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
     }
     if (a.scores && real) {
       float* out = a.scores + t * a.experts + first;
-      for (int p0 = 0; p0 < mine; p0 += 4) {
-        if (P > 4 || a.sigmoid) e = four(p0, [&](double v) { return (double)score32(v, a.sigmoid, s_top, s_inv); });
+      for (int from = 0; from < mine; from += at.step) {
+        if (P > 4 || a.sigmoid) e = four(from, [&](double v) { return (double)score32(v, a.sigmoid, s_top, s_inv); });
         const bool unscaled = P <= 4 && !a.sigmoid;
         const float v[4] = {(float)(unscaled ? e.a * s_inv : e.a), (float)(unscaled ? e.b * s_inv : e.b), (float)(unscaled ? e.c * s_inv : e.c),
                             (float)(unscaled ? e.d * s_inv : e.d)};
-        st_float4(out + p0, v, mine - p0, false);
+        st_float4(out + from, v, mine - from, false);
       }
     }
     double s = chosen >= 0 ? score_of(as_logit(logit), a.sigmoid, s_top, s_inv) : 0.0;
