@@ -88,6 +88,22 @@ def test_norm_of_the_longest_rows():
     assert repeats(y, (x[:PERIOD].float() * rstd).to(BF)) and untouched(yb)
 
 
+def test_norm_gradient_of_the_longest_row():
+    """One row of 2^30 - 1 columns: dw is dy t itself, dx its formula with a sum over all of them."""
+    n = 2 ** 30 - 1
+    h, dy, rstd = repeated(n, 5), repeated(n, 6), torch.full((1,), 0.875, device="cuda:0")
+    w = torch.ones(n, dtype=BF, device="cuda:0")
+    (xb, dx), (wb, dw) = guarded(n, BF), guarded(n, F32)
+    need = fp8q.load_library().fp8q_rmsnorm_backward_workspace(1, n)
+    work = torch.empty(need // 4, device="cuda:0")
+    call("fp8q_rmsnorm_backward", dy, 1, 1, n, n, h, 1, n, rstd, w, 1, None, n, dx, 1, n, 0, None, n, None, dw, work, need)
+    t = h[:PERIOD].float() * rstd
+    assert repeats(dw, dy[:PERIOD].float() * t) and untouched(wb) and untouched(xb)
+    dot = sum((dy[i:i + (1 << 26)].double() * h[i:i + (1 << 26)].double()).sum().item() for i in range(0, n, 1 << 26))
+    mean = torch.tensor(dot * 0.875 / n, dtype=F32, device="cuda:0")
+    assert repeats(dx, ((dy[:PERIOD].float() - t * mean) * rstd).to(BF))
+
+
 def test_token_tiles_of_the_most_rows():
     rows = 128 * (2 ** 24 - 1)
     h, w, (rb, rstd) = repeated(rows, 3), torch.full((1,), 0.75, device="cuda:0"), guarded(rows, F32)
