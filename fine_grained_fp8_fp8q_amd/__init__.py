@@ -518,28 +518,15 @@ def _raw_stream(dev):
     return _stream_handle(dev.index)
 
 
-_current_device = None
-
-
-def _device_index():
-    """The current device, without the look at torch's initialization that
-    current_device takes (a tensor is on the GPU already) where torch has the
-    call for that."""
-    global _current_device
-    if _current_device is None:
-        torch = _torch()
-        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    return _current_device()
-
-
 def _call(dev, name, *args):
     """Calls the entry point on the current stream of dev, which becomes the
     current device for the call where it is not."""
+    torch = _torch()
     fn = getattr(_lib or load_library(), name)
-    if dev.index == _device_index():
+    if dev.index == torch.cuda.current_device():
         st = fn(*args, _raw_stream(dev))
     else:
-        with _torch().cuda.device(dev):
+        with torch.cuda.device(dev):
             st = fn(*args, _raw_stream(dev))
     if st != OK:
         raise Fp8qError(st, name)
