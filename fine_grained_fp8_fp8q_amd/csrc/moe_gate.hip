@@ -10,7 +10,7 @@
 // rounded.
 //
 // The batch of 16384 tokens, eight of 256 experts in four of eight groups, takes
-// 13.6 us (the bytes 2.8, the launch 2.6): 1200 vector instructions for the four
+// 13.6 us (the bytes 2.8, the launch 2.6): 1210 vector instructions for the four
 // tokens of a wave, all of whose 4096 start, load and choose at the same time.
 // One token takes 4.5 us.
 //
