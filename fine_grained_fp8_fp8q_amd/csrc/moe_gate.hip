@@ -99,8 +99,14 @@ __device__ __forceinline__ double exp64(double x) {
 }
 
 // Score of a logit; softmax: top the row's largest, inv 1 / sum exp(x - top).
+// Below -700 a sigmoid is exp(x), 1 + exp(-x) leaves the range before its
+// reciprocal does.
 __device__ __forceinline__ double score_of(double x, bool sigmoid, double top, double inv) {
-  if (sigmoid) return 1.0 / (1.0 + exp64(-x));
+  if (sigmoid) {
+    const bool far = x < -700.0;
+    const double t = exp64(far ? x : -x);
+    return far ? t : 1.0 / (1.0 + t);
+  }
   return x > kNone ? exp64(x - top) * inv : 0.0;
 }
 
@@ -185,11 +191,27 @@ __device__ __forceinline__ void gate_wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A token's scores may all be so small that 64 bits hold them in few bits, or
+// not at all: relative to the largest one they still have their shares of the
+// sum.  (So far below zero a sigmoid is exp(x), as a softmax's numerator is.)
+constexpr double kFarScores = 0x1p-900;
+__device__ __forceinline__ bool far_scores(double total, bool sigmoid) { return total < kFarScores && (!sigmoid || total > 0.0); }
+
 // What lane j of a token's lanes does with its j-th expert (-1: none).
 template <int L>
 __device__ __forceinline__ void gate_write(const GateArgs& a, int64_t t, bool real, int lane, int chosen, double w) {
   if (a.renormalize) {
-    const double total = gate_sum<L>(w);
+    double total = gate_sum<L>(w);
+    if (__builtin_amdgcn_ballot_w64(chosen >= 0 && far_scores(total, a.sigmoid))) {
+      const double x = chosen >= 0 ? as_logit(ld_logit(a.logits, a.lf32, t * a.ld + chosen)) : kNone;
+      const double top = gate_max<L>(x);
+      const double e = chosen >= 0 ? exp64(x - top) : 0.0;
+      const double sum = gate_sum<L>(e);
+      if (far_scores(total, a.sigmoid)) {
+        w = e;
+        total = sum;
+      }
+    }
     w = total > 0.0 ? w / total : 0.0;
   }
   if (real && lane < a.topk) {

@@ -553,8 +553,11 @@ fp8q_status fp8q_rmsnorm_quantize_t(const void* h, int h_dtype, int64_t h_rows, 
  * index.  Written per token, best first:
  *   experts[t, j]  the j-th best open expert, int32 or int64 (index_dtype)
  *   weights[t, j]  scale * s, or with renormalize scale * s / (sum of s over
- *                  the token's chosen experts), rounded to float32; 0 where
- *                  that sum is 0
+ *                  the token's chosen experts), rounded to float32.  That
+ *                  quotient stays what the formula gives where 64 bits no
+ *                  longer hold the scores well: a softmax's is one of the
+ *                  chosen logits alone, a sigmoid's is 0 only where all of the
+ *                  chosen scores are 0 in 64 bits (logits below -745)
  *   scores[t, e]   float32 [tokens, E], where the pointer is not NULL
  *   load[e]        int32 [E], where the pointer is not NULL: the number of
  *                  pairs that chose e is added to it

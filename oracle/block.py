@@ -89,6 +89,20 @@ def scores(x, score):
     return x, e / math.fsum(e)
 
 
+def shares(x, s, score):
+    """What each of a token's chosen logits x, of scores s, has of the sum of their scores: in extended precision and
+    relative to the largest, since 64 bits hold a score near e^-745 in few bits and below it not at all.  0 where every
+    score of a sigmoid is 0 in 64 bits; those of a softmax have a sum whatever else is in the row."""
+    if len(x) == 0 or (score == "sigmoid" and not np.any(s)):
+        return np.zeros(len(x))
+    wide = np.asarray(x, dtype=np.longdouble)
+    low = np.minimum(wide, 0) if score == "sigmoid" else wide
+    e = np.exp(low - low.max())
+    if score == "sigmoid":
+        e = e / (1 + np.exp(-np.abs(wide)))
+    return np.asarray(e / e.sum(), dtype=np.float64)
+
+
 def route(logits, topk, bias=None, score="sigmoid", groups=1, top_groups=1, group_score="top2", renormalize=True, scale=1.0):
     """(experts int64 [tokens, topk], weights float64, scores float64 [tokens, E])."""
     tokens, n = logits.shape
@@ -110,9 +124,7 @@ def route(logits, topk, bias=None, score="sigmoid", groups=1, top_groups=1, grou
             key = np.array([key[i] if i // (n // groups) in opened else -np.inf for i in range(n)])
         order = [i for i in sorted(range(n), key=lambda i: (-key[i], i)) if key[i] > -np.inf][:topk]
         experts[t, :len(order)] = order
-        w = s[order]
-        total = math.fsum(w)
-        weights[t, :len(order)] = scale * (w if not renormalize else w / total if total > 0 else 0 * w)
+        weights[t, :len(order)] = scale * (shares(x[order], s[order], score) if renormalize else s[order])
     return experts, weights, every
 
 
