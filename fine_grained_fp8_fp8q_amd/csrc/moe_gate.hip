@@ -581,13 +581,14 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
 }
 
 // ------------------------------------------------------------- gradient ---
-// With ds_e = d loss / d s_e,
-//   renormalised  ds_e = scale (dw_e - sum_k dw_k s_k / S) / S, S = sum of the chosen scores,
-//   else          ds_e = scale dw_e,
-// plus dscores; dx = ds s (1 - s), or s (ds - sum over all experts of ds s).
-// Of the renormalised softmax that sum is 0: its weights are a softmax of the
-// chosen logits alone.  Every step is in 64 bits: what is left of a difference
-// may be little.
+// With the chosen scores s_k, S their sum and w_k = s_k / S, the gradient that
+// the weights bring to a chosen logit is
+//   renormalised  scale w_k (dw_k - sum_j dw_j w_j), of a sigmoid times (1 - s_k),
+//   else          scale dw_k s_k (1 - s_k), or scale s_k (dw_k - sum_j dw_j s_j);
+// dscores add ds s (1 - s), or s (ds - sum over all experts of ds s).  1 / S is
+// never formed alone: it may leave the range where w_k does not.  (The
+// renormalised softmax needs the chosen logits alone.)  Every step is in 64
+// bits: what is left of a difference may be little.
 
 // What lane j of a token's lanes knows of its j-th choice: the expert (-1:
 // none), the gradient of its weight (0 without one) and its logit.
@@ -629,18 +630,37 @@ __device__ __forceinline__ double gate_same(double v, int e, int topk) {
   return sum;
 }
 
-// A sigmoid and its slope s (1 - s) = t / (1 + t)^2, t = e^-|x|.  1 + t is in
-// [1, 2]: its reciprocal needs no scaling, and two Newton steps after the
+// A sigmoid, 1 - s, and its slope s (1 - s) = t / (1 + t)^2, t = e^-|x|.  1 + t
+// is in [1, 2]: its reciprocal needs no scaling, and two Newton steps after the
 // approximate one (half the cost of a division).
 struct Sigmoid {
-  double s, slope;
+  double s, rest, slope;
 };
 __device__ __forceinline__ Sigmoid sigmoid64(double x) {
   const double t = exp64(-fabs(x)), d = 1.0 + t;
   double r = __builtin_amdgcn_rcp(d);
   r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
   r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-  return {x < 0.0 ? t * r : r, t * r * r};
+  return {x < 0.0 ? t * r : r, x < 0.0 ? r : t * r, t * r * r};
+}
+
+// w_k (dw_k - sum_j dw_j w_j) of a token's choices, s their scores.
+template <int L>
+__device__ __forceinline__ double gate_share_gradient(const GateChoice& c, double s, bool sigmoid) {
+  const bool live = c.x > kNone;
+  if (!live) s = 0.0;
+  double total = gate_sum<L>(s), dot = gate_sum<L>(live ? c.dw * s : 0.0);
+  if (__builtin_amdgcn_ballot_w64(live && far_scores(total, sigmoid))) {
+    const double top = gate_max<L>(c.x), e = live ? exp64(c.x - top) : 0.0;
+    const double sum = gate_sum<L>(e), edot = gate_sum<L>(live ? c.dw * e : 0.0);
+    if (far_scores(total, sigmoid)) {
+      s = e;
+      total = sum;
+      dot = edot;
+    }
+  }
+  const double inv = total > 0.0 ? 1.0 / total : 0.0;  // (2^900 at most, or of a sum of 1 or more)
+  return s * inv * (c.dw - dot * inv);
 }
 
 // Where only the chosen experts have a gradient (a sigmoid, or the renormalised
@@ -665,14 +685,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_few_kernel(GateBwdAr
     double dx;
     if (a.sigmoid) {
       const Sigmoid y = sigmoid64(c.x);
-      double ds = c.dw;
-      if (a.renormalize) {
-        const double s = c.x > kNone ? y.s : 0.0;
-        const double total = gate_sum<L>(s), dot = gate_sum<L>(c.x > kNone ? c.dw * s : 0.0);
-        const double inv = total > 0.0 ? 1.0 / total : 0.0;
-        ds = (c.dw - dot * inv) * inv;
-      }
-      dx = a.scale * ds * y.slope;
+      dx = a.scale * (a.renormalize ? gate_share_gradient<L>(c, y.s, true) * y.rest : c.dw * y.slope);
     } else {
       const double top = gate_max<L>(c.x);
       const double e = c.x > kNone ? exp64(c.x - top) : 0.0;
@@ -700,7 +713,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_few_kernel(GateBwdAr
   }
 }
 
-// Every expert: a lane has P consecutive ones, the chosen ones' ds comes to it
+// Every expert: a lane has P consecutive ones, the chosen ones' part comes to it
 // through LDS, where the lanes' p-th values lie side by side.  Bound by the
 // exponentials of every expert in 64 bits (16384 x 256: 19 us, the bytes 8).
 template <int L, int P>
@@ -754,27 +767,30 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_all_kernel(GateBwdAr
 #pragma unroll
       for (int p = 0; p < P; ++p) s[p] *= inv;
     }
-    const double mine = c.e >= 0 ? score_of(c.x, a.sigmoid, top, inv) : 0.0;
-    double ds = c.dw;
-    if (a.renormalize) {
-      const double total = gate_sum<L>(mine), dot = gate_sum<L>(c.e >= 0 ? c.dw * mine : 0.0);
-      ds = total > 0.0 ? (c.dw - dot / total) / total : 0.0;
+    // the chosen logits' part, a softmax's without its mean
+    double dx;
+    if (a.sigmoid) {
+      const Sigmoid y = sigmoid64(c.x);
+      dx = a.renormalize ? gate_share_gradient<L>(c, y.s, true) * y.rest : c.dw * y.slope;
+    } else {
+      const double mine = score_of(c.x, false, top, inv);
+      dx = a.renormalize ? gate_share_gradient<L>(c, mine, false) : c.dw * mine;
     }
-    ds = c.x > kNone ? a.scale * ds : 0.0;
+    dx = c.x > kNone ? a.scale * dx : 0.0;
     double mean = 0.0;
     if (!a.sigmoid) {
-      mean = c.e >= 0 ? ds * mine : 0.0;
+      if (!a.renormalize) mean = dx;
 #pragma unroll
       for (int p = 0; p < P; ++p)
         if (s[p] > 0.0) mean += (double)g[p] * s[p];
       mean = gate_sum<L>(mean);
     }
-    ds = gate_same<L>(ds, c.e, a.topk);
-    if (c.e >= 0) r[c.e % P * L + c.e / P] = ds;
+    dx = gate_same<L>(dx, c.e, a.topk);
+    if (c.e >= 0) r[c.e % P * L + c.e / P] = dx;
     gate_wave_fence();
     float d[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) d[p] = s[p] > 0.0 ? (float)((r[p * L + lane] + (double)g[p] - mean) * s[p]) : 0.0f;
+    for (int p = 0; p < P; ++p) d[p] = (float)(r[p * L + lane] + (s[p] > 0.0 ? ((double)g[p] - mean) * s[p] : 0.0));
     gate_wave_fence();
     if (!real) continue;
 #pragma unroll

@@ -577,7 +577,8 @@ fp8q_status fp8q_moe_route(const void* logits, int logits_dtype, int64_t tokens,
  * logits, the choice held fixed:
  *   ds[e] = sum over j with experts[t, j] = e of scale * dweights[t, j], or with
  *           renormalize of scale * (dweights[t, j] - sum_k dweights[t, k] w_k) / S
- *           (S the sum of the chosen scores, w_k = s_k / S; 0 where S is 0)
+ *           (S the sum of the chosen scores, w_k = s_k / S as fp8q_moe_route has
+ *           it; where it has 0 for all of them, so is this)
  *   plus dscores[t, e] (float32 [tokens, E]; may be NULL)
  *   sigmoid: dlogits = ds * s * (1 - s),  softmax: dlogits = s * (ds - sum_e ds * s)
  * over E logits as for fp8q_moe_route, with its score, renormalize and scale.

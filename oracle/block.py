@@ -93,7 +93,7 @@ def shares(x, s, score):
     """What each of a token's chosen logits x, of scores s, has of the sum of their scores: in extended precision and
     relative to the largest, since 64 bits hold a score near e^-745 in few bits and below it not at all.  0 where every
     score of a sigmoid is 0 in 64 bits; those of a softmax have a sum whatever else is in the row."""
-    if len(x) == 0 or (score == "sigmoid" and not np.any(s)):
+    if not np.any(np.isfinite(x)) or (score == "sigmoid" and not np.any(s)):
         return np.zeros(len(x))
     wide = np.asarray(x, dtype=np.longdouble)
     low = np.minimum(wide, 0) if score == "sigmoid" else wide
@@ -137,19 +137,25 @@ def route_backward(dweights, experts, logits, score="sigmoid", renormalize=True,
         ds = np.zeros(n) if dscores is None else np.array(dscores[t], dtype=np.float64)
         size = np.abs(ds)
         at = [(int(e), float(d)) for e, d in zip(experts[t], dweights[t]) if 0 <= e < n]
-        total = math.fsum(s[e] for e, _ in at)
+        # what renormalised weights w = s / S bring to x_k is w_k (dw_k - sum_j dw_j w_j), a sigmoid's times 1 - s_k: S itself
+        # may be far below what can be divided by
+        own, own_size = np.zeros(n), np.zeros(n)
+        picked = [e for e, _ in at]
+        w = shares(x[picked], s[picked], score) if renormalize else []
+        mean = math.fsum(d * v for (_, d), v in zip(at, w))
+        mean_size = math.fsum(abs(d) * v for (_, d), v in zip(at, w))
+        rest = np.array([0.0 if v == -np.inf else scores(np.array([-v]), "sigmoid")[1][0] for v in x]) if score == "sigmoid" else np.ones(n)  # 1 - s
         for e, d in at:
             if not renormalize:
                 ds[e] += scale * d
                 size[e] += abs(scale * d)
-            elif total > 0:
-                ds[e] += scale * (d - math.fsum(k * s[j] for j, k in at) / total) / total
-                size[e] += abs(scale) * (abs(d) + math.fsum(abs(k) * s[j] for j, k in at) / total) / total
+        for (e, d), v in zip(at, w):
+            own[e] += scale * v * (d - mean) * rest[e]
+            own_size[e] += abs(scale) * v * (abs(d) + mean_size) * rest[e]
         live = x > -np.inf
-        ds, size = np.where(live, ds, 0.0), np.where(live, size, 0.0)
+        ds, size, own, own_size = (np.where(live, v, 0.0) for v in (ds, size, own, own_size))
         if score == "sigmoid":
-            slope = s * np.array([0.0 if v == -np.inf else scores(np.array([-v]), "sigmoid")[1][0] for v in x])
-            dx[t], mag[t] = ds * slope, size * slope
+            dx[t], mag[t] = own + ds * (s * rest), own_size + size * (s * rest)
         else:
-            dx[t], mag[t] = s * (ds - math.fsum(ds * s)), s * (size + math.fsum(size * s))
+            dx[t], mag[t] = own + s * (ds - math.fsum(ds * s)), own_size + s * (size + math.fsum(size * s))
     return dx, mag

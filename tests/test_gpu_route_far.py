@@ -72,3 +72,39 @@ def test_route_orders_scores_below_the_normal_numbers():
         want = np.exp(np.array([0, -0.5, -1, -9]))
         want /= want.sum()
         assert (np.abs(host(w.double()) - want) <= NEAR32 * want).all()
+
+
+@pytest.mark.parametrize("n,topk", [(8, 2), (60, 4), (256, 8), (128, 16), (300, 17), (512, 64)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_route_backward_of_far_scores(n, topk, score, renormalize):
+    r = np.random.default_rng(n + topk)
+    x = far_logits(r, n)
+    if score == "softmax":
+        x[:38, ::7] = 0.0
+    e = np.stack([r.permutation(n)[:topk] for _ in range(40)])
+    if score == "softmax":  # the near ones are not chosen: every chosen score is far
+        e = np.stack([r.permutation(np.setdiff1d(np.arange(n), np.arange(0, n, 7)))[:topk] for _ in range(40)])
+    e[3, 1], e[36, 0], e[35, 1] = e[3, 0], -1, n
+    dw = r.normal(size=(40, topk)).astype(np.float32)
+    for dscores in (None, r.normal(size=(40, n)).astype(np.float32)):
+        want, mag = B.route_backward(dw, e, x, score, renormalize, 2.5, dscores)
+        assert np.isfinite(want).all() and (not renormalize or np.abs(want[20:24]).max() > 1e-3)
+        # 64-bit steps of the magnitudes that are added, a hundred or so of them, and the rounding of the result
+        bound = 2.0 ** -24 * 1.01 * np.abs(want) + 200 * 2.0 ** -53 * mag + 2.0 ** -134
+        for tokens in TOKENS:
+            rows = np.arange(tokens) % 40 if tokens > 1 else np.array([24])
+            got = host(fp8q.moe_route_backward(dev(dw[rows]), dev(e[rows]), dev(x[rows]), score=score, renormalize=renormalize, scale=2.5,
+                                               dscores=None if dscores is None else dev(dscores[rows])).double())
+            assert (np.abs(got - want[rows]) <= bound[rows]).all(), (tokens, dscores is None)
+
+
+def test_route_and_its_gradient_agree_on_far_scores():
+    """Weights by the forward pass, moved by differences of the oracle's, against the gradient: two far logits."""
+    x, dw = np.array([[-720.0, -720.5, -900.0]], dtype=np.float32), np.array([[1.0, -0.3]], dtype=np.float32)
+    e, w, _ = fp8q.moe_route(dev(x), 2, scale=2.5)
+    share = host(w.double())[0] / 2.5
+    want = 2.5 * share[0] * share[1] * 1.3
+    for dscores in (None, torch.zeros((1, 3), device="cuda:0")):
+        got = host(fp8q.moe_route_backward(dev(dw), e, dev(x), scale=2.5, dscores=dscores).double())[0]
+        assert np.allclose(got, [want, -want, 0], rtol=1e-6, atol=0) and abs(want - 0.764) < 1e-3

@@ -45,3 +45,34 @@ def test_scores_that_are_zero_in_64_bits():
     w = B.route(x, 2, bias, score="softmax")[1][0]
     assert abs(w[0] + w[1] - 1) < 1e-15 and abs(w[1] / np.exp(-54.0) - 1) < 1e-14
     assert B.route(np.full((1, 3), -np.inf), 2)[1].tolist() == [[0.0, 0.0]]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("far", FAR)
+def test_gradient_of_far_scores(far, score):
+    """Against the formula in decimals, and the weights' central differences in decimals."""
+    x = np.array([far + [0.0, 1.0]])
+    n, k = x.shape[1], len(far)
+    r = np.random.default_rng(k)
+    dw, ds = r.normal(size=(1, k)), r.normal(size=(1, n))
+    experts = np.arange(k)[None]
+
+    def loss(at):
+        s = [1 / (1 + (-v).exp()) for v in at]
+        if score == "softmax":
+            e = [v.exp() for v in at]
+            s = [v / sum(e) for v in e]
+        total = sum(s[:k])
+        return sum(Decimal(2.5) * Decimal(float(d)) * v / total for d, v in zip(dw[0], s)) + sum(Decimal(float(d)) * v for d, v in zip(ds[0], s))
+
+    dx, mag = B.route_backward(dw, experts, x, score, True, 2.5, ds)
+    with localcontext() as c:
+        c.prec = 400  # (a share of e^-743 = 10^-323 beside one of 1 moves the sum in its 323rd digit)
+        at, step = [Decimal(float(v)) for v in x[0]], Decimal(10) ** -12
+        for i in range(n):
+            up, down = list(at), list(at)
+            up[i] += step
+            down[i] -= step
+            want = float((loss(up) - loss(down)) / (2 * step))
+            # a central difference of step 1e-12 is off by 1e-24 of the third derivative, a few of the magnitudes summed
+            assert abs(dx[0, i] - want) <= 1e-13 * mag[0, i] + 3 * 2.0 ** -1074, i
