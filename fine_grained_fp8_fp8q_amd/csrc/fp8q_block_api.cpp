@@ -71,6 +71,8 @@ fp8q_status fp8q_rmsnorm_backward(const void* dy, int dy_dtype, int64_t rows, in
   if (rows > 0 && (!dy || !h || !rstd || ((dx || dx_codes) && !weight) || (dx_codes && !dx_scales))) return FP8Q_ERR_INVALID_ARG;
   if (N >= kMaxRow || (rows > 0 && (ld_dy < N || ld_h < N || (dresidual && ld_dresidual < N) || (dx && ld_dx < N) || (dx_codes && ld_codes < N))))
     return FP8Q_ERR_SHAPE;
+  // (as the stream over its own input: at another stride dx would overwrite rows of dresidual that are still to be read)
+  if (dx && dx == dresidual && ld_dx != ld_dresidual && rows > 1) return FP8Q_ERR_SHAPE;
   const int64_t need = dweight ? fp8q_rmsnorm_backward_workspace(rows, N) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need)) return FP8Q_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(h) || !aligned16(rstd) || !aligned16(weight) || !aligned16(dresidual) || !aligned16(dx) ||

@@ -484,7 +484,7 @@ fp8q_status fp8q_grouped_wgrad_ex(const uint8_t* dy_t, const float* dy_scales,
  * fp8q_quantize_act(FP8Q_TILE_ROW, scale_mode) writes for that y.  The
  * outputs of a row do not depend on the other rows nor on their number.  h
  * may be residual itself with the same stride (the stream is then updated in
- * place).  eps > 0 and finite.  Infinities and NaN follow float32 arithmetic
+ * place; another stride gives FP8Q_ERR_SHAPE).  eps > 0 and finite.  Infinities and NaN follow float32 arithmetic
  * in h, rstd and y of their row; for the codes every y must be finite.  rstd
  * keeps its precision while it is a normal float32 number (a root of the mean
  * square below 2^126).  With N = 0 rstd is rn32(1 / sqrt(eps)).  N < 2^30,
@@ -506,7 +506,7 @@ fp8q_status fp8q_rmsnorm_quantize(const void* x, int x_dtype, int64_t rows, int6
  * rounding (dx_codes [rows, ld_codes >= N], dx_scales [rows, ceil(N/128)],
  * scale_mode) and dweight [N] are each written where the pointer is not NULL;
  * one at least must be given.  dx may be dresidual itself with the same
- * stride.  Without rows dweight is zero.  dweight is summed in an order that
+ * stride (another one gives FP8Q_ERR_SHAPE).  Without rows dweight is zero.  dweight is summed in an order that
  * depends on the sizes alone.  workspace: DEVICE memory of at least
  * fp8q_rmsnorm_backward_workspace(rows, N) bytes for dweight (without it 0:
  * it may be NULL), used until the call's work is done; calls that may run at

@@ -1,0 +1,33 @@
+"""Calls at the edges of what the entry points between a block's linear layers
+accept, on the CPU: what is refused before anything touches the GPU, and sizes
+that the host works out."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+import fine_grained_fp8_fp8q_amd as fp8q
+
+P, Q = ctypes.c_void_p(4096), ctypes.c_void_p(8192)  # never dereferenced
+REACHED = fp8q.ERR_DEVICE  # accepted, without a GPU
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(fp8q.LIB_PATH):
+        pytest.skip("libfp8q.so is not built")
+    return fp8q.load_library()
+
+
+def test_dx_over_dresidual_at_another_stride_is_refused(lib):
+    """A workgroup's rows of dx would land on rows of dresidual that another has yet to read."""
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls would run")
+    # 0 dy, dtype, rows, N, ld, 5 h, dtype, ld, 8 rstd, weight, dtype, 11 dres, ld, 13 dx, dtype, ld, 16 mode, codes, ld, scales, 20 dweight, workspace, bytes, stream
+    for rows, dres, ldr, dx, ldx, status in ((4, P, 16, P, 8, fp8q.ERR_SHAPE), (4, P, 8, P, 16, fp8q.ERR_SHAPE), (2, P, 9, P, 8, fp8q.ERR_SHAPE), (4, P, 16, P, 16, REACHED),
+                                             (4, P, 16, Q, 8, REACHED), (1, P, 16, P, 8, REACHED), (4, P, 16, None, 8, REACHED)):
+        codes = None if dx else Q
+        args = [Q, 1, rows, 8, 8, Q, 1, 8, Q, Q, 1, dres, ldr, dx, 1, ldx, 0, codes, 8, codes, None, None, 0, None]
+        assert lib.fp8q_rmsnorm_backward(*args) == status, (rows, ldr, ldx)
