@@ -53,7 +53,7 @@ fp8q_status fp8q_rmsnorm_quantize(const void* x, int x_dtype, int64_t rows, int6
 
 int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t N) {
   if (!dim_ok(rows) || !dim_ok(N) || N >= kMaxRow || rows == 0 || N == 0) return 0;
-  return fp8q::norm_bwd_blocks((int)rows) * fp8q::norm_partial_ld((int)N) * (int64_t)sizeof(float);
+  return fp8q::norm_bwd_blocks((int)rows, (int)N) * fp8q::norm_partial_ld((int)N) * (int64_t)sizeof(float);
 }
 
 fp8q_status fp8q_rmsnorm_backward(const void* dy, int dy_dtype, int64_t rows, int64_t N, int64_t ld_dy, const void* h, int h_dtype,

@@ -192,7 +192,7 @@ inline int norm_threads(int n, int chunks) {
 }
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 // dres == nullptr: no such term; dx, codes, dweight == nullptr: not written.
-// partial: float [norm_bwd_blocks(rows), norm_partial_ld(n)], only used for
+// partial: float [norm_bwd_blocks(rows, n), norm_partial_ld(n)], only used for
 // dweight.
 struct NormBwdArgs {
   const void* dy;
@@ -246,8 +246,11 @@ inline NormBwdShape norm_bwd_shape(int rows, int n, bool f32) {
   s.blocks = (int)(want < blocks ? want : blocks);
   return s;
 }
-// blocks of the workspace: no shape has more
-inline int norm_bwd_blocks(int rows) { return rows < kNormBwdBlocks ? rows : kNormBwdBlocks; }
+// blocks of the workspace: those of the types that take more
+inline int norm_bwd_blocks(int rows, int n) {
+  const int b = norm_bwd_shape(rows, n, false).blocks, f = norm_bwd_shape(rows, n, true).blocks;
+  return b > f ? b : f;
+}
 inline int64_t norm_partial_ld(int n) { return ((int64_t)n + 7) / 8 * 8; }
 hipError_t launch_norm_backward(const NormBwdArgs& a, hipStream_t stream);
 // index == nullptr: row t of the output is row t of h

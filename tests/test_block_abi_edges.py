@@ -31,3 +31,10 @@ def test_dx_over_dresidual_at_another_stride_is_refused(lib):
         codes = None if dx else Q
         args = [Q, 1, rows, 8, 8, Q, 1, 8, Q, Q, 1, dres, ldr, dx, 1, ldx, 0, codes, 8, codes, None, None, 0, None]
         assert lib.fp8q_rmsnorm_backward(*args) == status, (rows, ldr, ldx)
+
+
+def test_gradients_workspace_holds_the_shares_that_are_written(lib):
+    """A share a workgroup, or of rows beyond a workgroup's registers one of every 32 rows: not one of every row."""
+    need = lib.fp8q_rmsnorm_backward_workspace
+    for rows, n, shares in ((8192, 7168, 256), (512, 20000, 16), (64, 1 << 29, 2), (1, 16385, 1), (33, 40000, 2), (1 << 20, 40000, 512), (100000, 512, 512), (5, 512, 5), (8192, 7169, 512)):
+        assert need(rows, n) == shares * ((n + 7) // 8 * 8) * 4, (rows, n)
