@@ -246,6 +246,8 @@ inline NormBwdShape norm_bwd_shape(int rows, int n, bool f32) {
   s.blocks = (int)(want < blocks ? want : blocks);
   return s;
 }
+// rows of each of `blocks` blocks (rows reach 2^31 - 1: their sum with the blocks is not a 32-bit number)
+inline int norm_dw_rows(int rows, int blocks) { return (int)(((int64_t)rows + blocks - 1) / blocks); }
 // blocks of the workspace: those of the types that take more
 inline int norm_bwd_blocks(int rows, int n) {
   const int b = norm_bwd_shape(rows, n, false).blocks, f = norm_bwd_shape(rows, n, true).blocks;

@@ -274,7 +274,7 @@ static void launch_norm_bwd_typed(const NormBwdArgs& a, hipStream_t stream) {
     if (a.dx || a.codes)
       hipLaunchKernelGGL((norm_bwd_long_kernel<DF32, HF32, OF32>), dim3(a.rows < kMaxNormGrid ? a.rows : kMaxNormGrid), dim3(kMaxNormThreads), 0, stream, a);
     if (a.dweight) {
-      const int per = (a.rows + s.blocks - 1) / s.blocks;
+      const int per = norm_dw_rows(a.rows, s.blocks);
       hipLaunchKernelGGL((norm_dw_kernel<DF32, HF32>), dim3((a.n + kNormThreads - 1) / kNormThreads, s.blocks), dim3(kNormThreads), 0, stream, a, per);
     }
     return;

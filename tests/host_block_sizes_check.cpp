@@ -1,0 +1,26 @@
+// Sizes that the host works out for the kernels between a block's linear
+// layers, at the largest row counts; built for the CPU with AddressSanitizer
+// and UndefinedBehaviorSanitizer by tests/test_block_abi_edges.py.  Prints
+// "host block size checks passed" and returns 0 when every check holds.
+#include <cstdint>
+#include <cstdio>
+
+#include "fp8q_internal.h"
+
+int main() {
+  int failures = 0;
+  for (int64_t rows : {int64_t(1), int64_t(33), int64_t(129), int64_t(16385), (int64_t(1) << 31) - 512, (int64_t(1) << 31) - 1})
+    for (int n : {8193, 16385, 1 << 29})
+      for (bool f32 : {false, true}) {
+        const fp8q::NormBwdShape s = fp8q::norm_bwd_shape((int)rows, n, f32);
+        if (s.chunks != 0) continue;  // (a row in registers)
+        const int64_t per = fp8q::norm_dw_rows((int)rows, s.blocks);
+        // the blocks' rows are all there are, and no block begins before the one ahead of it
+        if (!(per >= 1 && per * s.blocks >= rows && (per - 1) * s.blocks < rows)) {
+          std::printf("rows %lld, %d columns, %d blocks: %lld rows each\n", (long long)rows, n, s.blocks, (long long)per);
+          ++failures;
+        }
+      }
+  if (failures == 0) std::printf("host block size checks passed\n");
+  return failures != 0;
+}
