@@ -180,6 +180,7 @@ struct NormArgs {
 // 8.7 / 7.3 / 7.5, one row 3.9 / 3.7 / 4.0; 16384 x 4096 87 / 79 / 80; 16384 x
 // 2048 44.8 / 42.8 / 43.1, one row 2.7 / 3.0 / 3.6; 65536 x 512 44 / 52 / 84.
 constexpr int kMaxNormRow = 16384;
+constexpr int kMaxNormGrid = 1 << 20;  // workgroups; more rows go round
 inline int norm_chunks(int rows, int n) {
   const int items = (n + 7) / 8;
   if (items <= (rows < 4096 ? 256 : 128)) return 1;
@@ -189,6 +190,16 @@ inline int norm_threads(int n, int chunks) {
   if (n > kMaxNormRow) return 0;
   const int per = ((n + 7) / 8 + chunks - 1) / chunks;
   return per == 0 ? 64 : (per + 63) / 64 * 64;
+}
+// Where many rows of the same width have twice the chunks, few have twice their
+// threads (split), so that the sum over a row is the same.
+struct NormShape {
+  int chunks, threads;
+  bool split;
+};
+inline NormShape norm_shape(int rows, int n) {
+  const int chunks = norm_chunks(rows, n), most = norm_chunks(kMaxNormGrid, n);
+  return {chunks, norm_threads(n, most) * (most / chunks), chunks != most};
 }
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 // dres == nullptr: no such term; dx, codes, dweight == nullptr: not written.
@@ -232,7 +243,6 @@ struct NormBwdShape {
   int threads, chunks, blocks;
   bool wave;
 };
-constexpr int kMaxNormGrid = 1 << 20;  // workgroups; more rows go round
 constexpr int kNormBwdBlocks = 512;
 inline NormBwdShape norm_bwd_shape(int rows, int n, bool f32) {
   const int items = (n + 7) / 8, most = f32 ? 2 : 4;

@@ -20,12 +20,12 @@ enum { kNoStream = 0, kStreamBF16 = 1, kStreamF32 = 2 };
 // do, 20 a value: 82 us, where the bytes take 55; BF16 out 80, the bytes 73.
 // One row takes 3.6 us, 2.6 of them the launch: of the rest most is two loads
 // and a barrier in a row, one after another.
-template <bool XF32, int STREAM, bool VEC, bool KEEP, int CH>
+template <bool XF32, int STREAM, bool VEC, bool KEEP, int CH, bool SPLIT>
 __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) void norm_row_kernel(NormArgs a) {
   static_assert(VEC || KEEP, "loads of unaligned rows are plain ones");
   constexpr bool RES = STREAM != kNoStream, HF32 = RES ? STREAM == kStreamF32 : XF32;
   __shared__ double part[kMaxNormThreads / 64];
-  const int tid = threadIdx.x, step = (int)blockDim.x * 8;
+  const int tid = SPLIT ? split_thread() : (int)threadIdx.x, step = (int)blockDim.x * 8;
   const bool out = a.y || a.codes;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     Raw<HF32, 8> h[CH];
@@ -60,18 +60,23 @@ __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) vo
       }
     }
     const Row<HF32, VEC> rh(a.h, row * a.ldh, a.n);
-    double sum = 0.0;
+    double sums[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      sums[c] = 0.0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const double v = (double)h[c].at(i);
-        sum = __builtin_fma(v, v, sum);
+        sums[c] = __builtin_fma(v, v, sums[c]);
       }
       forget(h[c]);
       if (RES && a.h) rh.store(c * step + tid * 8, h[c]);
     }
-    const float r = reciprocal_rms(block_sum(sum, part), a.inv_n, a.eps);
+    // (the halves of the row's threads apart, as few rows have them)
+    double sum = sums[0];
+    if constexpr (CH == 2) sum += sums[1];
+    if constexpr (CH == 4) sum = (sums[0] + sums[2]) + (sums[1] + sums[3]);
+    const float r = reciprocal_rms(SPLIT ? split_sum(sum, part) : block_sum(sum, part), a.inv_n, a.eps);
     if (tid == 0 && a.rstd) a.rstd[row] = r;
     if (out) {
       const Row<false, VEC> ry(a.y, row * a.ldy, a.n);
@@ -152,32 +157,33 @@ __global__ __launch_bounds__(kMaxNormThreads) void norm_long_kernel(NormArgs a) 
 static int norm_grid(int rows) { return rows < kMaxNormGrid ? rows : kMaxNormGrid; }
 
 template <bool XF32, int STREAM, bool VEC, bool KEEP>
-static void launch_norm_rows(const NormArgs& a, int threads, int chunks, hipStream_t stream) {
-  auto kernel = chunks == 1   ? norm_row_kernel<XF32, STREAM, VEC, KEEP, 1>
-                : chunks == 2 ? norm_row_kernel<XF32, STREAM, VEC, KEEP, 2>
-                              : norm_row_kernel<XF32, STREAM, VEC, KEEP, 4>;
-  hipLaunchKernelGGL(kernel, dim3(norm_grid(a.rows)), dim3(threads), 0, stream, a);
+static void launch_norm_rows(const NormArgs& a, const NormShape& s, hipStream_t stream) {
+  auto kernel = s.split ? (s.chunks == 1 ? norm_row_kernel<XF32, STREAM, VEC, KEEP, 1, true> : norm_row_kernel<XF32, STREAM, VEC, KEEP, 2, true>)
+                : s.chunks == 1 ? norm_row_kernel<XF32, STREAM, VEC, KEEP, 1, false>
+                : s.chunks == 2 ? norm_row_kernel<XF32, STREAM, VEC, KEEP, 2, false>
+                                : norm_row_kernel<XF32, STREAM, VEC, KEEP, 4, false>;
+  hipLaunchKernelGGL(kernel, dim3(norm_grid(a.rows)), dim3(s.threads), 0, stream, a);
 }
 
 template <bool XF32, int STREAM>
 static void launch_norm_typed(const NormArgs& a, hipStream_t stream) {
   const bool vec = a.n % 8 == 0 && a.ldx % 8 == 0 && (!a.res || a.ldr % 8 == 0) && (!a.h || a.ldh % 8 == 0) && (!a.y || a.ldy % 8 == 0) &&
                    (!a.codes || a.ldc % 8 == 0);
-  const int chunks = norm_chunks(a.rows, a.n), threads = norm_threads(a.n, chunks);
-  if (threads == 0) {
+  const NormShape s = norm_shape(a.rows, a.n);
+  if (s.threads == 0) {
     hipLaunchKernelGGL((norm_long_kernel<XF32, STREAM>), dim3(norm_grid(a.rows)), dim3(kMaxNormThreads), 0, stream, a);
     return;
   }
   if constexpr (!XF32 && STREAM != kStreamF32) {
     if (vec && !input_stays_cached(a.rows, (int64_t)a.n * (STREAM == kNoStream ? 2 : 4))) {
-      launch_norm_rows<XF32, STREAM, true, false>(a, threads, chunks, stream);
+      launch_norm_rows<XF32, STREAM, true, false>(a, s, stream);
       return;
     }
   }
   if (vec) {
-    launch_norm_rows<XF32, STREAM, true, true>(a, threads, chunks, stream);
+    launch_norm_rows<XF32, STREAM, true, true>(a, s, stream);
   } else {
-    launch_norm_rows<XF32, STREAM, false, true>(a, threads, chunks, stream);
+    launch_norm_rows<XF32, STREAM, false, true>(a, s, stream);
   }
 }
 

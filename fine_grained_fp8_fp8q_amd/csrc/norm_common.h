@@ -2,13 +2,13 @@
 // row, rounded the same way everywhere, and sums over a wave.
 //
 // With r = 1 / sqrt(mean(h^2) + eps), the sum in 64 bits and r rounded once to
-// float32, a row's output is y = bf16(fl(fl(h r) w)).  A 64-bit sum differs
-// between two orders of addition by some 2^-50, so r, and with it every bit of
-// y, of its codes and of its scales, is the same whichever way the row is
-// split over threads, in the forward pass and wherever y is formed again.  (A
-// float32 sum moves r by a step now and then, and with it a tile's scale by a
-// step of BF16.)  The 64-bit steps are two of
-// some twenty instructions a value.
+// float32, a row's output is y = bf16(fl(fl(h r) w)).  The sum's order depends on
+// the row's width alone, not on the number of rows, by which its split over
+// threads goes (split_sum, norm_bwd_shape): so r, and with it every bit of y, of
+// its codes and of its scales, is that of the row alone.  (In another order a
+// 64-bit sum differs by some 2^-50, which moves r by a step seldom, but not
+// never; a float32 sum moves r now and then, and with it a tile's scale by a
+// step of BF16.)  The 64-bit steps are two of some twenty instructions a value.
 #pragma once
 
 #include "chunk8.h"
@@ -199,6 +199,34 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
   __syncthreads();
   double t = part[0];
   for (int i = 1; i < (int)blockDim.x >> 6; ++i) t += part[i];
+  return t;
+}
+
+// Where few rows go to twice the threads of many, each with half the chunks, a
+// thread's place in the row: of 32 lanes the first 16 have a tile of the row's
+// first half of threads, the others the one that many rows give the same
+// threads.  So the two halves of such a thread's sum are 16 lanes apart.
+__device__ __forceinline__ int split_thread() {
+  const int tid = threadIdx.x;
+  return (tid >> 5) * 16 + (tid & 15) + (tid & 16 ? (int)blockDim.x >> 1 : 0);
+}
+// block_sum of what those threads would have of many rows, bit for bit: first
+// the two halves, then a wave's two tiles, then two waves, which are one there.
+__device__ __forceinline__ double split_sum(double v, double* part) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  // (of x and x: the even one of two times 16 lanes in both, and the odd one in both)
+  const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  v += dpp_double<0xB1>(v);
+  v += dpp_double<0x4E>(v);
+  v += dpp_double<0x141>(v);
+  v += dpp_double<0x140>(v);
+  const double s = lane_double(v, 0) + lane_double(v, 32);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  double t = part[0] + part[1];
+  for (int i = 2; i < (int)blockDim.x >> 6; i += 2) t += part[i] + part[i + 1];
   return t;
 }
 

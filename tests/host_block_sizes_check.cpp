@@ -21,6 +21,18 @@ int main() {
           ++failures;
         }
       }
+  // the forward pass: every width is held by the threads, and few rows' have what many rows' have in half as many with twice the chunks
+  for (int n : {0, 1, 512, 1024, 1025, 1030, 1536, 2048, 2049, 4096, 4097, 7168, 8193, 16384})
+    for (int rows : {1, 2047, 2048, 4095, 4096, 1 << 21, 2147483647}) {
+      const fp8q::NormShape s = fp8q::norm_shape(rows, n), many = fp8q::norm_shape(2147483647, n);
+      const bool holds = (int64_t)s.threads * s.chunks * 8 >= n && s.threads % 64 == 0 && s.threads >= 64 && s.threads <= (s.chunks == 4 ? 512 : 1024);
+      const bool same = s.split ? s.chunks <= 2 && s.threads % 128 == 0 && s.threads == 2 * many.threads && 2 * s.chunks == many.chunks
+                                : s.threads == many.threads && s.chunks == many.chunks;
+      if (!holds || !same || many.split) {
+        std::printf("%d rows, %d columns: %d chunks of %d threads, many rows %d of %d\n", rows, n, s.chunks, s.threads, many.chunks, many.threads);
+        ++failures;
+      }
+    }
   if (failures == 0) std::printf("host block size checks passed\n");
   return failures != 0;
 }
