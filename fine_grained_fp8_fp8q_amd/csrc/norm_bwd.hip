@@ -32,9 +32,16 @@ struct NormBwdRow {
 // fills; its codes too 108), the two launches where they are few (one row 6.9
 // us), and the vector instructions where rows begin anywhere (their ends are
 // shifted into place: 4096 x 7001 70 us, the bytes 36).
+// Three chunks a lane with float32 values are held to the registers of two waves
+// a SIMD: float32 dy and dx beside BF16 h on unaligned rows need four more
+// (8192 x 1030 34.7 us with those spilled, 38.4 with one wave).
 template <bool DF32, bool HF32, bool OF32, bool VEC, bool KEEP, int CH, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 512) void norm_bwd_rows_kernel(NormBwdArgs a) {
-  __shared__ double part[2][kMaxNormThreads / 64];
+__global__ __launch_bounds__(WAVE ? 256 : 512, WAVE && CH == 3 && (DF32 || HF32 || OF32) ? 2 : 1) void norm_bwd_rows_kernel(NormBwdArgs a) {
+  // Rows of 129 to 192 chunks with float32 values go to a wave each or to
+  // workgroups of two, by their number.  Both add a lane's chunks 128 apart, then
+  // those 64 apart, which are the two waves', then the lanes: the same sum.
+  constexpr bool kApart = (DF32 || HF32 || OF32) && CH == (WAVE ? 3 : 2);
+  __shared__ double part[2][kApart && !WAVE ? 128 : kMaxNormThreads / 64];
   __shared__ __attribute__((aligned(16))) float4 share[WAVE ? kSlots * CH * 128 : 1];
   const int slot = WAVE ? (int)threadIdx.x >> 6 : 0, tid = WAVE ? (int)threadIdx.x & 63 : (int)threadIdx.x;
   const int lanes = WAVE ? 64 : (int)blockDim.x, slots = WAVE ? (int)blockDim.x >> 6 : 1, step = lanes * 8;
@@ -76,7 +83,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_bwd_rows_kernel(NormBwd
     const float r = v.r;
     double sum = 0.0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
+    for (int k = 0; k < CH; ++k) {
+      const int c = kApart && WAVE ? (3 - k) % 3 : k;  // (0, 2, 1: two sums at a time)
+      const double before = sum;
+      if (kApart) sum = 0.0;
       Row<DF32, VEC>(a.dy, 0, a.n).settle(c * step + tid * 8, v.dy[c]);
       Row<HF32, VEC>(a.h, 0, a.n).settle(c * step + tid * 8, v.h[c]);
       Row<OF32, VEC>(a.dres, 0, a.n).settle(c * step + tid * 8, v.res[c]);
@@ -86,20 +96,28 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_bwd_rows_kernel(NormBwd
         dw[c][i] = __builtin_fmaf(d, h * r, dw[c][i]);
         sum = __builtin_fma((double)(d * w[c][i]), (double)h, sum);
       }
+      if (kApart) sum = before + sum;
       // (the sum is formed here, not where it is used with every widened value alive until then)
       asm volatile("" : "+v"(sum));
       forget(v.dy[c]);
       forget(v.h[c]);
     }
     if (a.dx || a.codes) {
-      sum = wave_sum(sum);
-      if constexpr (!WAVE) {
-        // two sets of partial sums in turn: a wave two rows ahead has passed the barrier in between
-        if ((tid & 63) == 0) part[turn][tid >> 6] = sum;
+      if (kApart && !WAVE && lanes == 128) {
+        part[turn][tid] = sum;
         __syncthreads();
-        sum = part[turn][0];
-        for (int i = 1; i < lanes >> 6; ++i) sum += part[turn][i];
+        sum = wave_sum(sum + part[turn][tid ^ 64]);
         turn ^= 1;
+      } else {
+        sum = wave_sum(sum);
+        if constexpr (!WAVE) {
+          // two sets of partial sums in turn: a wave two rows ahead has passed the barrier in between
+          if ((tid & 63) == 0) part[turn][tid >> 6] = sum;
+          __syncthreads();
+          sum = part[turn][0];
+          for (int i = 1; i < lanes >> 6; ++i) sum += part[turn][i];
+          turn ^= 1;
+        }
       }
       const float mean = (float)(sum * (double)r * a.inv_n);
       const Row<OF32, VEC> dx(a.dx, row * a.lddx, a.n, a.dx != nullptr);

@@ -1,6 +1,7 @@
 """A row's results do not depend on the other rows nor on their number: rows
-whose 1 / rms lies so close to the border between two float32 values that
-another order of the 64-bit sum would round it the other way, alone and in batches of every size at which the kernels change."""
+whose 1 / rms, or whose mean in the gradient, lies so close to the border
+between two float32 values that another order of the 64-bit sum would round it
+the other way, alone and in batches of every size at which the kernels change."""
 
 import numpy as np
 import pytest
@@ -68,4 +69,41 @@ def test_norm_of_a_row_is_that_of_the_row_alone(n, pad, residual):
         many.copy_(x[pick])
         for i, v in enumerate(norm(many)):
             bad = torch.nonzero((v != want[i][pick]).reshape(rows, -1).any(1)).flatten()
+            assert bad.numel() == 0, (rows, i, bad.numel(), bad[0].item())
+
+
+def gradients_at_a_border(r, n):
+    """(dy, h), float32, of positive terms whose mean is within a few 64-bit steps of a border."""
+    h, dy = np.abs(r.normal(size=(ROWS, n))).astype(np.float32), np.abs(r.normal(size=(ROWS, n))).astype(np.float32)
+    first = r.integers(0, n - 1, size=ROWS)
+    for t in range(ROWS):
+        i = first[t]
+        h[t, i], h[t, i + 1], dy[t, i], dy[t, i + 1] = 1, 2.0 ** -20, 0, 0
+        rest = (dy[t].astype(np.longdouble) * h[t].astype(np.longdouble)).sum()
+        border = (np.longdouble(np.float32(rest / n)) + np.longdouble(np.nextafter(np.float32(rest / n), np.float32(9)))) / 2
+        lacks = border * n - rest + np.longdouble(r.uniform(-3, 3) * 2.0 ** -52) * rest
+        dy[t, i] = np.float32(lacks)
+        dy[t, i + 1] = np.float32((lacks - np.longdouble(dy[t, i])) * 2 ** 20)
+    return dy, h
+
+
+@pytest.mark.parametrize("n,pad", [(1030, 0), (1032, 0), (1536, 0), (1536, 1), (2048, 0), (7168, 0), (520, 0)])
+@pytest.mark.parametrize("odt", [F32, BF])
+def test_gradient_of_a_row_is_that_of_the_row_alone(n, pad, odt):
+    r = np.random.default_rng(n + pad)
+    values = gradients_at_a_border(r, n)
+    w = torch.ones(n, device="cuda:0")
+
+    def grad(pick):
+        t = [torch.zeros((len(pick), n + pad), device="cuda:0")[:, :n].copy_(dev(v[pick])) for v in values]
+        return fp8q.rmsnorm_backward(t[0], t[1], torch.ones(len(pick), device="cuda:0"), w, out_dtype=odt, quantize=True, want_dweight=False)[:3]
+
+    want = grad(np.arange(ROWS))
+    alone = [grad(np.array([t])) for t in range(20)]
+    for i, v in enumerate(want):
+        assert torch.equal(v[:20], torch.cat([a[i] for a in alone])), i
+    for rows in (600, 1600, 2047, 2048, 4096):
+        pick = np.arange(rows) % ROWS
+        for i, v in enumerate(grad(pick)):
+            bad = torch.nonzero((v != want[i][dev(pick)]).reshape(rows, -1).any(1)).flatten()
             assert bad.numel() == 0, (rows, i, bad.numel(), bad[0].item())
