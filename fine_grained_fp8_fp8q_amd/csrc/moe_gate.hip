@@ -36,31 +36,16 @@ __device__ __forceinline__ float ld_logit(const void* p, bool f32, int64_t i) {
 // A logit as it is used: NaN is none (-inf), +inf the largest number.
 __device__ __forceinline__ double as_logit(float x) { return x == x ? (double)fminf(x, 3.402823466e38f) : kNone; }
 
-// The value of another lane of the same 16, by a DPP control.
-template <int CTRL>
-__device__ __forceinline__ double gate_dpp(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-__device__ __forceinline__ double gate_lane(double v, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
 // f over a token's L lanes (16: one DPP row, 32: two, or the whole wave), the
 // same in each.  All 64 lanes must be active.
 template <int L, class F>
 __device__ __forceinline__ double gate_all(double v, F f) {
-  v = f(v, gate_dpp<0xB1>(v));
-  v = f(v, gate_dpp<0x4E>(v));
-  v = f(v, gate_dpp<0x141>(v));
-  v = f(v, gate_dpp<0x140>(v));
+  v = f(v, dpp_double<0xB1>(v));
+  v = f(v, dpp_double<0x4E>(v));
+  v = f(v, dpp_double<0x141>(v));
+  v = f(v, dpp_double<0x140>(v));
   if constexpr (L == 32) v = f(v, __shfl_xor(v, 16));
-  if constexpr (L == 64) v = f(f(gate_lane(v, 0), gate_lane(v, 16)), f(gate_lane(v, 32), gate_lane(v, 48)));
+  if constexpr (L == 64) v = f(f(lane_double(v, 0), lane_double(v, 16)), f(lane_double(v, 32), lane_double(v, 48)));
   return v;
 }
 template <int L>

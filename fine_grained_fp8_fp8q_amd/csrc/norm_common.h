@@ -166,20 +166,6 @@ __device__ __forceinline__ void widen_gain8(const Gain8& g, bool f32, int col, i
 // y before its rounding to BF16.
 __device__ __forceinline__ float normalised(float h, float r, float w) { return (h * r) * w; }
 
-// A double of the lane that a DPP control names.
-template <int CTRL>
-__device__ __forceinline__ double dpp_double(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double lane_double(double v, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
 // Sum over the wave, the same in every lane: within rows of 16 lanes by DPP
 // (as dpp_max16), then the four rows' sums.  All 64 lanes must be active.
 __device__ __forceinline__ double wave_sum(double v) {

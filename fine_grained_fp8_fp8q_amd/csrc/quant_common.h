@@ -57,6 +57,21 @@ __device__ __forceinline__ uint32_t dpp_max16(uint32_t v) {
   return v;
 }
 
+// A double of the lane that a DPP control names.
+template <int CTRL>
+__device__ __forceinline__ double dpp_double(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// A double of a lane that is the same for the whole wave.
+__device__ __forceinline__ double lane_double(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // float32 -> BF16 bit pattern, round to nearest even (finite inputs).
 __device__ __forceinline__ uint32_t bf16_rne_bits(float f) {
   const uint32_t u = __float_as_uint(f);
