@@ -803,6 +803,15 @@ def _vector(t, n, dtypes, name):
     return t.data_ptr()
 
 
+def _on16(t, addr):
+    """t and its address, or those of a copy that begins on a 16-byte boundary:
+    micro-batches slice per-row vectors anywhere, the library reads them from there."""
+    if addr is None or addr & 15 == 0:
+        return t, addr
+    t = t.clone()
+    return t, t.data_ptr()
+
+
 def rmsnorm_quantize(x, weight, residual=None, eps=1e-6, bf16=False, quantize=True, scale_mode="free", h_out=None):
     """Residual addition, RMS norm and 1x128 quantization of its output.
 
@@ -854,7 +863,8 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, out_dtype=None, quantize=Fa
     its type out_dtype (torch.bfloat16 by default, dres's type with one).
     Returns (dx, codes, scales, dweight), None for what was not asked for: dx
     [rows, N] (want_dx), the 1x128 quantization of its BF16 rounding
-    (quantize) and float32 dweight [N] (want_dweight).
+    (quantize) and float32 dweight [N] (want_dweight).  rstd may be a slice of
+    a batch's anywhere (off a 16-byte boundary it is copied first).
     """
     torch = _torch()
     f32, b16 = types = _types()[1]
@@ -863,6 +873,7 @@ def rmsnorm_backward(dy, h, rstd, weight, dres=None, out_dtype=None, quantize=Fa
     if (hr, hn) != (rows, n):
         raise ValueError(f"h must be [{rows}, {n}], got [{hr}, {hn}]")
     rstd_p, w_p = _vector(rstd, rows, (f32,), "rstd"), _vector(weight, n, types, "weight")
+    rstd, rstd_p = _on16(rstd, rstd_p)
     res_p, ldr = None, n
     if dres is not None:
         rr, rn, ldr, res_p = _rows_of(dres, "dres", types if out_dtype is None else (out_dtype,))
@@ -899,15 +910,17 @@ def rmsnorm_quantize_t(h, rstd, weight, index=None, scale_mode="free"):
     of the y that ``rmsnorm_quantize`` forms.
 
     index: int32 [rows], the row of h behind every row of the token axis
-    (``moe_sort``'s token; outside h: zeros).  Default: every row of h.
+    (``moe_sort``'s token; outside h: zeros).  Default: every row of h.  rstd
+    and index may be slices anywhere, as for ``rmsnorm_backward``.
     """
     types = _types()[1]
     hr, n, ldh, h_p = _rows_of(h, "h", types)
     rstd_p, w_p = _vector(rstd, hr, types[:1], "rstd"), _vector(weight, n, types, "weight")
+    rstd, rstd_p = _on16(rstd, rstd_p)
     rows, i_p = hr, None
     if index is not None:
         rows = index.numel() if isinstance(index, _types()[0]) else 0
-        i_p = _vector(index, rows, _types()[2:], "index")
+        index, i_p = _on16(index, _vector(index, rows, _types()[2:], "index"))
     dev = _one_device(h, rstd, weight, index)
     codes, ldc = _new_codes(n, rows, dev)
     scales = _new(n, (rows + 127) // 128, types[0], dev)
@@ -970,7 +983,8 @@ def moe_route_backward(dweights, experts, logits, score="sigmoid", renormalize=T
     choice held fixed: dweights float32 and experts (int32 or int64) [tokens,
     topk], logits, score, renormalize and scale as there.  dscores: float32
     [tokens, E], added as the gradient of the scores.  Returns dlogits
-    [tokens, E], out_dtype or the logits' type.
+    [tokens, E], out_dtype or the logits' type.  dweights and experts may be
+    rows of a batch's anywhere, as rstd for ``rmsnorm_backward``.
     """
     torch = _torch()
     tensor, types, i32 = _types()
@@ -992,7 +1006,8 @@ def moe_route_backward(dweights, experts, logits, score="sigmoid", renormalize=T
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     dev = _one_device(logits, dweights, experts, dscores)
     dlogits = _new(tokens, n, out_dtype, dev)
-    _call(dev, "fp8q_moe_route_backward", _addr(dweights), _addr(experts), INDEX_I32 if experts.dtype == i32 else INDEX_I64, tokens,
+    (dweights, dw_p), (experts, e_p) = _on16(dweights, dweights.data_ptr()), _on16(experts, experts.data_ptr())
+    _call(dev, "fp8q_moe_route_backward", dw_p, e_p, INDEX_I32 if experts.dtype == i32 else INDEX_I64, tokens,
           shape[1], logits_p, types.index(logits.dtype), n, ld, _score(score), bool(renormalize), scale, _addr(dscores), _addr(dlogits),
           types.index(out_dtype), n)
     return dlogits
