@@ -838,7 +838,7 @@ int gate_grid(int64_t waves) {
 
 template <int L, int BY>
 static void launch_gate_by(const GateArgs& a, int per, hipStream_t stream) {
-  // (of 32 lanes each has more than eight, or 16 would do)
+  // (of 32 lanes nearly always more than four each: experts or choices enough that 16 would not do)
   auto kernel = L == 32 ? gate_kernel<L, kGateLane, BY> : per <= 4 ? gate_kernel<L, L == 32 ? kGateLane : 4, BY>
                 : per <= 8 ? gate_kernel<L, L == 32 ? kGateLane : 8, BY> : gate_kernel<L, kGateLane, BY>;
   const int64_t waves = ((int64_t)a.tokens * L + 63) / 64;
@@ -857,13 +857,26 @@ static void launch_gate_lanes(const GateArgs& a, int per, hipStream_t stream) {
 
 // Four tokens a wave take less time in all, one a wave less for each: of 256
 // experts, 2048 tokens 7.4 against 6.8 us, 4099 8.8 against 9.5, 16384 13.2
-// against 22.7; of 60, 1024 tokens 3.6 against 3.9, 16384 5.5 against 15.4.  The
-// scores of all experts, which are written in 64-bit steps, are many for a lane
-// of few: 4099 tokens of 160 11.4 against 8.5, 16384 19.2 against 23.3.
+// against 22.7; of 60, 1024 tokens 3.6 against 3.9, 16384 5.5 against 15.4.
+// Where the scores of all experts are written, in 64-bit steps, few lanes have
+// many of them to do: of 60, 1024 tokens 5.0 against 5.3, 4096 5.2 against 8.6;
+// of 128, 2048 8.0 against 7.2, 4096 7.1 against 8.7 (a softmax 7.8 against
+// 8.6); of 160, 4096 9.0 against 8.7, 8192 12.5 against 14.8 (12.6 against
+// 14.1); of 256, 4096 10.3 against 9.0, 8192 13.8 against 15.5 (a softmax 15.8
+// against 14.9), 16384 21.6 against 26.3 (23.1 against 25.5).
+static int gate_narrow_from(const GateArgs& a) {
+  if (!a.scores) return a.narrow.per <= 8 ? 1024 : 4096;
+  return a.narrow.per <= 4 ? 1024 : a.narrow.per <= 8 ? 4096 : a.narrow.per <= 12 || a.sigmoid ? 8192 : 16384;
+}
 // Two tokens a wave, where four would leave a lane more experts than its
 // registers hold: of 384 experts, 2048 tokens 7.1 against 6.6 with one, 4096 7.9
 // against 8.2, 16384 18.0 against 23.1; of 512, sixteen of them, 24 against 31.
-static int gate_narrow_from(const GateArgs& a) { return a.scores ? 16384 : a.narrow.per <= 8 ? 1024 : 4096; }
+// So where 16 lanes are too few for the choices, 15 to 30 of them, unless every
+// score is written as well; with a bias, whose unclear tokens cost more, only
+// from 16384 tokens on: sixteen of 256 by logits, 2048 tokens 6.7 against 5.8,
+// 4096 7.4 against 7.9, 16384 18.1 against 22.1; with a bias 4096 9.9 against
+// 9.1, 16384 22.6 against 23.9 (a softmax 13.6 against 11.7 and 26.3 against 27.5).
+static int gate_middle_from(const GateArgs& a) { return a.bias && a.narrow.fits ? 16384 : 4096; }
 
 // How `lanes` lanes a token share out the experts (GateLane).
 static GateSplit gate_split(const GateArgs& a, int lanes) {
@@ -892,7 +905,7 @@ hipError_t launch_gate(GateArgs a, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(gate_grid(a.tokens)), dim3(64 * kGateWaves), 0, stream, a);
   } else if (a.narrow.fits && a.topk + 2 <= 16 && a.tokens >= gate_narrow_from(a)) {
     launch_gate_lanes<16>(a, a.narrow.per, stream);
-  } else if (!a.narrow.fits && a.middle.fits && a.topk + 2 <= 32 && a.tokens >= 4096) {
+  } else if (a.middle.fits && a.topk + 2 <= 32 && (!a.narrow.fits || (a.topk + 2 > 16 && !a.scores)) && a.tokens >= gate_middle_from(a)) {
     launch_gate_lanes<32>(a, a.middle.per, stream);
   } else {
     launch_gate_lanes<64>(a, a.wide.per, stream);
