@@ -25,7 +25,7 @@ __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) vo
   static_assert(VEC || KEEP, "loads of unaligned rows are plain ones");
   constexpr bool RES = STREAM != kNoStream, HF32 = RES ? STREAM == kStreamF32 : XF32;
   __shared__ double part[kMaxNormThreads / 64];
-  const int tid = SPLIT ? split_thread() : (int)threadIdx.x, step = (int)blockDim.x * 8;
+  const int tid = SPLIT ? split_thread<CH>() : (int)threadIdx.x, step = (int)blockDim.x * 8;
   const bool out = a.y || a.codes;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     Raw<HF32, 8> h[CH];
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(CH == 4 ? kMaxNormThreads / 2 : kMaxNormThreads) vo
     double sum = sums[0];
     if constexpr (CH == 2) sum += sums[1];
     if constexpr (CH == 4) sum = (sums[0] + sums[2]) + (sums[1] + sums[3]);
-    const float r = reciprocal_rms(SPLIT ? split_sum(sum, part) : block_sum(sum, part), a.inv_n, a.eps);
+    const float r = reciprocal_rms(SPLIT ? split_sum<CH>(sum, part) : block_sum(sum, part), a.inv_n, a.eps);
     if (tid == 0 && a.rstd) a.rstd[row] = r;
     if (out) {
       const Row<false, VEC> ry(a.y, row * a.ldy, a.n);

@@ -191,27 +191,39 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
 // Where few rows go to twice the threads of many, each with half the chunks, a
 // thread's place in the row: of 32 lanes the first 16 have a tile of the row's
 // first half of threads, the others the one that many rows give the same
-// threads.  So the two halves of such a thread's sum are 16 lanes apart.
+// threads.  So the two halves of such a thread's sum are 16 lanes apart.  Of 192
+// threads (NormShape) the last wave's have no other half: 64 in their order.
+template <int CH>
+__device__ __forceinline__ bool three_waves() {
+  return CH == 1 && blockDim.x == 192;
+}
+template <int CH>
 __device__ __forceinline__ int split_thread() {
   const int tid = threadIdx.x;
-  return (tid >> 5) * 16 + (tid & 15) + (tid & 16 ? (int)blockDim.x >> 1 : 0);
+  if (three_waves<CH>() && tid >= 128) return tid - 64;
+  return (tid >> 5) * 16 + (tid & 15) + (tid & 16 ? three_waves<CH>() ? 128 : (int)blockDim.x >> 1 : 0);
 }
 // block_sum of what those threads would have of many rows, bit for bit: first
 // the two halves, then a wave's two tiles, then two waves, which are one there.
+template <int CH>
 __device__ __forceinline__ double split_sum(double v, double* part) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  // (of x and x: the even one of two times 16 lanes in both, and the odd one in both)
-  const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
-  const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
-  v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  const bool whole = three_waves<CH>() && threadIdx.x >= 128;
+  if (!whole) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    // (of x and x: the even one of two times 16 lanes in both, and the odd one in both)
+    const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  }
   v += dpp_double<0xB1>(v);
   v += dpp_double<0x4E>(v);
   v += dpp_double<0x141>(v);
   v += dpp_double<0x140>(v);
-  const double s = lane_double(v, 0) + lane_double(v, 32);
+  const double s = whole ? (lane_double(v, 0) + lane_double(v, 16)) + (lane_double(v, 32) + lane_double(v, 48)) : lane_double(v, 0) + lane_double(v, 32);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
   __syncthreads();
   double t = part[0] + part[1];
+  if (three_waves<CH>()) return t + part[2];
   for (int i = 2; i < (int)blockDim.x >> 6; i += 2) t += part[i] + part[i + 1];
   return t;
 }

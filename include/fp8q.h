@@ -506,11 +506,12 @@ fp8q_status fp8q_rmsnorm_quantize(const void* x, int x_dtype, int64_t rows, int6
  * rounding (dx_codes [rows, ld_codes >= N], dx_scales [rows, ceil(N/128)],
  * scale_mode) and dweight [N] are each written where the pointer is not NULL;
  * one at least must be given.  dx may be dresidual itself with the same
- * stride (another one gives FP8Q_ERR_SHAPE).  Without rows dweight is zero.  dweight is summed in an order that
- * depends on the sizes alone.  workspace: DEVICE memory of at least
- * fp8q_rmsnorm_backward_workspace(rows, N) bytes for dweight (without it 0:
- * it may be NULL), used until the call's work is done; calls that may run at
- * the same time need one each.  A missing or small workspace gives
+ * stride (another one gives FP8Q_ERR_SHAPE).  A row of dx and its codes do not
+ * depend on the other rows nor on their number.  Without rows dweight is zero.
+ * dweight is summed in an order that depends on the sizes alone.  workspace:
+ * DEVICE memory of at least fp8q_rmsnorm_backward_workspace(rows, N) bytes for
+ * dweight (without it 0: it may be NULL), used until the call's work is done;
+ * calls that may run at the same time need one each.  A missing or small workspace gives
  * FP8Q_ERR_INVALID_ARG.  Infinities and NaN follow float32 arithmetic in dx
  * and dweight; for the codes every dx must be a finite BF16 value.
  * N < 2^30, else FP8Q_ERR_SHAPE. */

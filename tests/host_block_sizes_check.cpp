@@ -26,7 +26,8 @@ int main() {
     for (int rows : {1, 2047, 2048, 4095, 4096, 1 << 21, 2147483647}) {
       const fp8q::NormShape s = fp8q::norm_shape(rows, n), many = fp8q::norm_shape(2147483647, n);
       const bool holds = (int64_t)s.threads * s.chunks * 8 >= n && s.threads % 64 == 0 && s.threads >= 64 && s.threads <= (s.chunks == 4 ? 512 : 1024);
-      const bool same = s.split ? s.chunks <= 2 && s.threads % 128 == 0 && s.threads == 2 * many.threads && 2 * s.chunks == many.chunks
+      const bool halves = s.threads == 2 * many.threads || (s.threads == 192 && many.threads == 128 && s.chunks == 1 && n <= 192 * 8);
+      const bool same = s.split ? s.chunks <= 2 && many.threads % 64 == 0 && halves && 2 * s.chunks == many.chunks
                                 : s.threads == many.threads && s.chunks == many.chunks;
       if (!holds || !same || many.split) {
         std::printf("%d rows, %d columns: %d chunks of %d threads, many rows %d of %d\n", rows, n, s.chunks, s.threads, many.chunks, many.threads);

@@ -48,7 +48,7 @@ def rows_at_a_border(r, n):
     return x
 
 
-@pytest.mark.parametrize("n,pad", [(1032, 0), (1030, 3), (2048, 0), (2048, 1), (4104, 0), (7168, 0), (7168, 5), (9000, 0), (16384, 0)])
+@pytest.mark.parametrize("n,pad", [(1032, 0), (1030, 3), (1280, 0), (1536, 0), (1535, 1), (1544, 0), (2048, 0), (2048, 1), (4104, 0), (7168, 0), (7168, 5), (9000, 0), (16384, 0)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm_of_a_row_is_that_of_the_row_alone(n, pad, residual):
     r = np.random.default_rng(n + pad)
