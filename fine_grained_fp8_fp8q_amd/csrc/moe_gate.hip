@@ -650,7 +650,7 @@ __device__ __forceinline__ double gate_share_gradient(const GateChoice& c, doubl
 
 // Where only the chosen experts have a gradient (a sigmoid, or the renormalised
 // softmax, without dscores): the row is laid out in LDS, zeros but for them, and
-// its logits are read at them alone.  L lanes a token.  16384 x 256 float32: 8.5
+// its logits are read at them alone.  L lanes a token.  16384 x 256 float32: 8.6
 // us, of which 2.6 are the launch and 2.5 the 17 MB that are written; the rest is
 // two loads that wait for one another and the 64-bit steps of one choice a lane.
 template <int L>
@@ -700,7 +700,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_few_kernel(GateBwdAr
 
 // Every expert: a lane has P consecutive ones, the chosen ones' part comes to it
 // through LDS, where the lanes' p-th values lie side by side.  Bound by the
-// exponentials of every expert in 64 bits (16384 x 256: 19 us, the bytes 8).
+// exponentials of every expert in 64 bits (16384 x 256: 20 us, the bytes 8).
 template <int L, int P>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_all_kernel(GateBwdArgs a) {
   extern __shared__ __attribute__((aligned(16))) double ds_rows[];

@@ -13,11 +13,12 @@ namespace {
 constexpr int kMaxNormThreads = 1024;
 enum { kNoStream = 0, kStreamBF16 = 1, kStreamF32 = 2 };
 
-// One workgroup per row, CH chunks of eight columns a thread (norm_chunks), the
-// row kept in registers: every byte is moved once.  With a residual HBM bounds
+// One workgroup per row, CH chunks of eight columns a thread (norm_shape), the
+// row kept in registers: every byte is moved once.  SPLIT: the threads hold
+// halves of what those of many rows hold (split_sum).  With a residual HBM bounds
 // it: 16384 x 7168 BF16 to E4M3 137-139 us, 6.0 TB/s at 4:3 reads to writes (127 us
 // at the rates of plain reads and fills).  Without one the vector instructions
-// do, 20 a value: 82 us, where the bytes take 55; BF16 out 80, the bytes 73.
+// do, 20 a value: 76-79 us, where the bytes take 55; BF16 out 79, the bytes 73.
 // One row takes 3.6 us, 2.6 of them the launch: of the rest most is two loads
 // and a barrier in a row, one after another.
 template <bool XF32, int STREAM, bool VEC, bool KEEP, int CH, bool SPLIT>
