@@ -234,8 +234,8 @@ struct NormBwdArgs {
 // them is float32): a wave a row while `chunks` of eight columns a lane hold
 // it, a workgroup above (chunks 0: the row is longer than that of 512 threads).
 // Three chunks of float32 values take the registers of two waves a SIMD: only
-// where there are rows enough (8192 rows of 1030 35 us, 43 by workgroups of two chunks a
-// thread; one row 7.3 and 6.6; the sums are the same bit for bit).
+// where there are rows enough (8192 rows of 1030 35 us, 43 by workgroups of two
+// chunks a thread; one row 7.3 and 6.5).  The sums are the same bit for bit.
 // `blocks` workgroups (of longer rows: blocks of them), each with a share of
 // the gain's gradient.  As few blocks as keep the memory busy, since every
 // share is written and read again: 8192 rows of 7168 BF16 columns take 87 us

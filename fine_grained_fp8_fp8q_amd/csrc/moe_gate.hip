@@ -570,10 +570,10 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a) {
 // the weights bring to a chosen logit is
 //   renormalised  scale w_k (dw_k - sum_j dw_j w_j), of a sigmoid times (1 - s_k),
 //   else          scale dw_k s_k (1 - s_k), or scale s_k (dw_k - sum_j dw_j s_j);
-// dscores add ds s (1 - s), or s (ds - sum over all experts of ds s).  1 / S is
-// never formed alone: it may leave the range where w_k does not.  (The
-// renormalised softmax needs the chosen logits alone.)  Every step is in 64
-// bits: what is left of a difference may be little.
+// dscores add ds s (1 - s), or s (ds - sum over all experts of ds s).  A 1 / S
+// that could leave the range, where w_k does not, is not formed (far_scores).
+// (The renormalised softmax needs the chosen logits alone.)  Every step is in
+// 64 bits: what is left of a difference may be little.
 
 // What lane j of a token's lanes knows of its j-th choice: the expert (-1:
 // none), the gradient of its weight (0 without one) and its logit.

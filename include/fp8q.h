@@ -484,11 +484,11 @@ fp8q_status fp8q_grouped_wgrad_ex(const uint8_t* dy_t, const float* dy_scales,
  * fp8q_quantize_act(FP8Q_TILE_ROW, scale_mode) writes for that y.  The
  * outputs of a row do not depend on the other rows nor on their number.  h
  * may be residual itself with the same stride (the stream is then updated in
- * place; another stride gives FP8Q_ERR_SHAPE).  eps > 0 and finite.  Infinities and NaN follow float32 arithmetic
- * in h, rstd and y of their row; for the codes every y must be finite.  rstd
- * keeps its precision while it is a normal float32 number (a root of the mean
- * square below 2^126).  With N = 0 rstd is rn32(1 / sqrt(eps)).  N < 2^30,
- * else FP8Q_ERR_SHAPE. */
+ * place; another stride gives FP8Q_ERR_SHAPE).  eps > 0 and finite.
+ * Infinities and NaN follow float32 arithmetic in h, rstd and y of their row;
+ * for the codes every y must be finite.  rstd keeps its precision while it is
+ * a normal float32 number (a root of the mean square below 2^126).  With N = 0
+ * rstd is rn32(1 / sqrt(eps)).  N < 2^30, else FP8Q_ERR_SHAPE. */
 fp8q_status fp8q_rmsnorm_quantize(const void* x, int x_dtype, int64_t rows, int64_t N, int64_t ld_x,
                                   const void* residual, int stream_dtype, int64_t ld_residual, void* h, int64_t ld_h,
                                   const void* weight, int weight_dtype, double eps, void* y_bf16, int64_t ld_y,
@@ -511,10 +511,10 @@ fp8q_status fp8q_rmsnorm_quantize(const void* x, int x_dtype, int64_t rows, int6
  * dweight is summed in an order that depends on the sizes alone.  workspace:
  * DEVICE memory of at least fp8q_rmsnorm_backward_workspace(rows, N) bytes for
  * dweight (without it 0: it may be NULL), used until the call's work is done;
- * calls that may run at the same time need one each.  A missing or small workspace gives
- * FP8Q_ERR_INVALID_ARG.  Infinities and NaN follow float32 arithmetic in dx
- * and dweight; for the codes every dx must be a finite BF16 value.
- * N < 2^30, else FP8Q_ERR_SHAPE. */
+ * calls that may run at the same time need one each.  A missing or small
+ * workspace gives FP8Q_ERR_INVALID_ARG.  Infinities and NaN follow float32
+ * arithmetic in dx and dweight; for the codes every dx must be a finite BF16
+ * value.  N < 2^30, else FP8Q_ERR_SHAPE. */
 int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t N);
 fp8q_status fp8q_rmsnorm_backward(const void* dy, int dy_dtype, int64_t rows, int64_t N, int64_t ld_dy,
                                   const void* h, int h_dtype, int64_t ld_h, const float* rstd,
